@@ -10,6 +10,11 @@ Entry points (same names as the C ABI):
         workspace (no workspace argument; the outputs are still the caller's or torch's)
     kda_prefill_workspace_bytes(...), kda_prefill_check(...), kda_prefill_plan(...)
     kda_status_string(status), kda_last_error(), kda_debug_check_cu_seqlens(cu, T)
+    kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, ...) -> (o, state_out):
+        linear attention with one decay per head (prefill and single tokens)
+    kda_pool_copy(pool, src, dst, ...), kda_pool_compact(pool, slots, ...): slots of a
+        state pool copied, forked, restored, cleared and compacted
+    kda_gated_norm(x, gate, weight, residual, ...): RMS norm, gate, residual and next norm
 """
 
 import ctypes
@@ -177,6 +182,15 @@ def load_library():
     lib.kda_debug_check_cu_seqlens.argtypes = [ctypes.c_void_p, ctypes.c_int64,
                                                ctypes.c_int64, ctypes.c_void_p]
     lib.kda_debug_check_cu_seqlens.restype = ctypes.c_int
+    for name in ("kda_linear", "kda_pool_copy", "kda_pool_compact", "kda_gated_norm"):
+        getattr(lib, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+        getattr(lib, name).restype = ctypes.c_int
+        getattr(lib, name + "_check").argtypes = [ctypes.c_void_p]
+        getattr(lib, name + "_check").restype = ctypes.c_int
+    for name in ("kda_linear_workspace_bytes", "kda_linear_plan",
+                 "kda_pool_compact_workspace_bytes"):
+        getattr(lib, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
+        getattr(lib, name).restype = ctypes.c_int
     lib.kda_abi_version.argtypes = []
     lib.kda_abi_version.restype = ctypes.c_int32
     if lib.kda_abi_version() != ABI_VERSION:
@@ -495,3 +509,12 @@ def kda_prefill_no_alloc(q, k, v, g, beta, state_in=None, cu_seqlens=None, **kw)
     if kw.get("workspace") is not None:
         raise KdaError(7, "kda_prefill_no_alloc takes no workspace")
     return kda_prefill(q, k, v, g, beta, state_in, cu_seqlens, _no_alloc=True, **kw)
+
+
+# The operators beside kda_prefill use the names above.
+from .linear import *  # noqa: E402,F401,F403
+from .norm import *  # noqa: E402,F401,F403
+from .pool import *  # noqa: E402,F401,F403
+from . import linear as _linear, norm as _norm, pool as _pool  # noqa: E402
+
+__all__ += _linear.__all__ + _norm.__all__ + _pool.__all__

@@ -16,8 +16,10 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libkda.so")
 
 SOURCES = ["kda_api.cpp", "kda_prepare.hip", "kda_recurrence.hip", "kda_fused.hip",
-           "kda_decode.hip"]
-HEADERS = ["kda_internal.h", "kda_device.h", "kda_recurrence_core.h", "kda_producer.h"]
+           "kda_decode.hip", "kda_ops_api.cpp", "kda_linear_chunks.hip",
+           "kda_linear_states.hip", "kda_linear_tokens.hip", "kda_pool.hip", "kda_norm.hip"]
+HEADERS = ["kda_internal.h", "kda_device.h", "kda_recurrence_core.h", "kda_producer.h",
+           "kda_ops_internal.h", "kda_linear_core.h"]
 
 FLAGS = [
     "--offload-arch=gfx950",

@@ -15,6 +15,7 @@
 
 #include "kda.h"
 #include "kda_internal.h"
+#include "kda_ops_internal.h"
 
 // Workspace of kda_prefill_no_alloc: one copy per device, alive until the process ends.
 // In host code this name is only a handle for hipGetSymbolAddress; the device address
@@ -373,6 +374,14 @@ kda_status scratch_on_current_device(void** out) {
 }
 
 }  // namespace
+
+kda_status kda::set_error(kda_status s, const char* text) noexcept {
+  try {
+    g_last_error = text;
+  } catch (...) {  // the status itself still says what failed
+  }
+  return s;
+}
 
 extern "C" {
 

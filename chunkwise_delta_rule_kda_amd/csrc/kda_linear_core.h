@@ -1,0 +1,347 @@
+// The chunked form of linear attention with one decay per head (device code).
+//
+// A chunk of C = 64 tokens that enters with the state S (V x K), with G_i the inclusive
+// prefix sum of its log decays:
+//   o_i = s exp(G_i) S q_i + s sum_{j <= i} exp(G_i - G_j) (q_i . k_j) v_j
+//   S'  = exp(G_C) S + sum_j exp(G_C - G_j) v_j k_j^T
+// Every exponent is a sum of log decays over some of the chunk's tokens, so no factor
+// passes 1 where the decays do not. The prefix sums are kept in FP64: their differences
+// are then exact to FP32 also behind a token that empties the state (-inf).
+//
+// One workgroup of four waves owns R = 64 NC value rows of one (segment, head) and walks
+// its chunks; each wave owns 16 NC of them with all keys, as MFMA accumulators
+// S[key][value] in registers, FP32. Everything is computed transposed (values or keys as
+// MFMA rows, tokens as columns), which lets the accumulators serve as operands without
+// any exchange between lanes:
+//   P^T tile (j, i)     = K . Q^T, scaled by its decays, through LDS to all waves
+//   O^T tile (value, i) = S^T Q^T (scaled by s exp(G_i)) + V^T P^T
+//   S tile (key, value) = exp(G_C) S + K^T (V exp(G_C - G_j))
+// Two 16-key accumulator tiles side by side hold keys 8 grp .. 8 grp + 7 of 32 in each
+// lane (the K^T operand's rows are permuted so), which is the operand order of a plain
+// 16-byte read of Q. For the contractions over tokens both sides use the order
+// kappa(kb, grp, e) = 32 kb + 16 (e / 4) + 4 grp + e % 4.
+//
+// LDS tiles are rows of 16-byte pieces, piece p of row r stored at p ^ (r % 16) (8-piece
+// rows: p ^ (r / 2 % 8)), so that the 16 rows an operand read touches lie in different
+// banks. BF16 operands that need eight tokens of one column come from the transposing LDS
+// read; FP32 ones (FP32 I/O) from 4-byte reads.
+#pragma once
+
+#include "kda_device.h"
+#include "kda_ops_internal.h"
+
+namespace kda {
+
+struct F32x8 {
+  f32x4 lo, hi;
+};
+
+template <bool BF16>
+struct FragOf {
+  typedef bf16x8 type;
+};
+template <>
+struct FragOf<false> {
+  typedef F32x8 type;
+};
+
+// C += A B over 32 contraction indices, eight per lane on each side in the same order.
+__device__ __forceinline__ f32x4 mma(bf16x8 a, bf16x8 b, f32x4 c) { return mfma32(a, b, c); }
+__device__ __forceinline__ f32x4 mma(const F32x8& a, const F32x8& b, f32x4 c) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.lo[e], b.lo[e], c, 0, 0, 0);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.hi[e], b.hi[e], c, 0, 0, 0);
+  return c;
+}
+
+__device__ __forceinline__ void to_frag(f32x4 lo, f32x4 hi, bf16x8& f) { f = pack8(lo, hi); }
+__device__ __forceinline__ void to_frag(f32x4 lo, f32x4 hi, F32x8& f) { f = F32x8{lo, hi}; }
+
+// Index (in 16-byte pieces) of piece p of row r in a tile of PPR pieces per row.
+template <int PPR>
+__device__ __forceinline__ int piece_at(int r, int p) {
+  static_assert(PPR == 8 || PPR == 16 || PPR == 32, "row sizes of 128, 256 or 512 bytes");
+  return r * PPR + (p ^ (PPR >= 16 ? (r & 15) : ((r >> 1) & 7)));
+}
+
+// Operand of row `row` (this lane's token) and its eight keys 32 kb + 8 grp ...
+template <int PPR>
+__device__ __forceinline__ void row_frag(const unsigned char* tile, int row, int kb, int grp,
+                                         bf16x8& f) {
+  f = *reinterpret_cast<const bf16x8*>(tile + 16 * piece_at<PPR>(row, 4 * kb + grp));
+}
+template <int PPR>
+__device__ __forceinline__ void row_frag(const unsigned char* tile, int row, int kb, int grp,
+                                         F32x8& f) {
+  f.lo = *reinterpret_cast<const f32x4*>(tile + 16 * piece_at<PPR>(row, 8 * kb + 2 * grp));
+  f.hi = *reinterpret_cast<const f32x4*>(tile + 16 * piece_at<PPR>(row, 8 * kb + 2 * grp + 1));
+}
+
+// Operand of one column and the eight tokens kappa(kb, grp, e). Lane m of 16 gets column
+// base + step * (m / 4) + m % 4: the transposing read takes four consecutive elements
+// from each of 16 lanes (lane i: row i / 4, column quad i % 4) and gives lane i element
+// i % 4 of quad i / 4 in all four rows.
+template <int PPR>
+__device__ __forceinline__ void col_frag(const unsigned char* tile, int base, int step, int kb,
+                                         int grp, int m, bf16x8& f) {
+  typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+  const int row = 32 * kb + 4 * grp + (m >> 2);
+  const int col = base + step * (m & 3);
+  const unsigned char* a = tile + 16 * piece_at<PPR>(row, col >> 3) + 2 * (col & 7);
+  const unsigned char* b = tile + 16 * piece_at<PPR>(row + 16, col >> 3) + 2 * (col & 7);
+  i16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)a);
+  i16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)b);
+  f = __builtin_shufflevector(__builtin_bit_cast(bf16x4, lo), __builtin_bit_cast(bf16x4, hi),
+                              0, 1, 2, 3, 4, 5, 6, 7);
+}
+template <int PPR>
+__device__ __forceinline__ void col_frag(const unsigned char* tile, int base, int step, int kb,
+                                         int grp, int m, F32x8& f) {
+  const int col = base + step * (m >> 2) + (m & 3);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const int row = 32 * kb + 4 * grp + e;
+    f.lo[e] = *reinterpret_cast<const float*>(tile + 16 * piece_at<PPR>(row, col >> 2) + 4 * (col & 3));
+    f.hi[e] = *reinterpret_cast<const float*>(tile + 16 * piece_at<PPR>(row + 16, col >> 2) + 4 * (col & 3));
+  }
+}
+
+// x scaled by one factor per token; with LOW also the part that rounding to BF16 leaves.
+template <bool LOW>
+__device__ __forceinline__ void scale_frag(bf16x8 x, f32x4 wlo, f32x4 whi, bf16x8& f, bf16x8& low) {
+  f32x4 lo, hi;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    lo[e] = static_cast<float>(x[e]) * wlo[e];
+    hi[e] = static_cast<float>(x[4 + e]) * whi[e];
+  }
+  f = pack8(lo, hi);
+  if constexpr (LOW) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      lo[e] -= static_cast<float>(f[e]);
+      hi[e] -= static_cast<float>(f[4 + e]);
+    }
+    low = pack8(lo, hi);
+  }
+}
+template <bool LOW>
+__device__ __forceinline__ void scale_frag(const F32x8& x, f32x4 wlo, f32x4 whi, F32x8& f, F32x8&) {
+  f.lo = x.lo * wlo;
+  f.hi = x.hi * whi;
+}
+
+// The decay factors of one chunk, in LDS.
+struct Gates {
+  double G[kLinChunk];  // inclusive prefix sums of the log2 decays
+  float a[kLinChunk];   // s * decay from the start of the token's 16-token block to it
+  float b[kLinChunk];   // decay from the token to the end of its block
+  float w[kLinChunk];   // decay from the token to the end of the chunk (0 behind the end)
+  float d[kLinChunk];   // s * decay from the start of the chunk to the token
+  float E[4];           // total decay of each block
+  float D;              // total decay of the chunk
+};
+
+constexpr double kLog2e = 1.4426950408889634074;
+
+// Log2 decay of token t of the chunk for head h; tok0 is the chunk's first token row.
+__device__ __forceinline__ double load_log_decay(const LinParams& p, int64_t tok0, int t, int left,
+                                                 int h) {
+  if (t >= left) return 0.0;
+  double x = 0.0;
+  if (p.g) {
+    const int64_t at = (tok0 + t) * p.H + h;
+    x = p.g_bf16 ? load1<true>(p.g, at) : load1<false>(p.g, at);
+  }
+  if (p.log_decay) x += static_cast<double>(p.log_decay[h]);
+  // -inf (an emptied state) as a finite number whose factor is 0; NaN stays
+  return (x < -1000.0 ? -1000.0 : x) * kLog2e;
+}
+
+// One wave, lane t = token t.
+__device__ __forceinline__ void make_gates(Gates& gt, double x, int t, int left, float scale) {
+  double G = x;
+#pragma unroll
+  for (int s = 1; s < 64; s <<= 1) {
+    const double y = __shfl_up(G, s);
+    if (t >= s) G += y;
+  }
+  const int blk = t & ~15;
+  const double before = __shfl(G, blk == 0 ? 0 : blk - 1);
+  const double start = blk == 0 ? 0.0 : before;
+  const double end = __shfl(G, blk + 15);
+  const double all = __shfl(G, 63);
+  gt.G[t] = G;
+  gt.a[t] = scale * __builtin_amdgcn_exp2f(static_cast<float>(G - start));
+  gt.b[t] = __builtin_amdgcn_exp2f(static_cast<float>(end - G));
+  gt.w[t] = t < left ? __builtin_amdgcn_exp2f(static_cast<float>(all - G)) : 0.f;
+  gt.d[t] = scale * __builtin_amdgcn_exp2f(static_cast<float>(G));
+  if ((t & 15) == 0) gt.E[t >> 4] = __builtin_amdgcn_exp2f(static_cast<float>(end - start));
+  if (t == 0) gt.D = __builtin_amdgcn_exp2f(static_cast<float>(all));
+}
+
+// A tile of 64 rows x PPR pieces between memory and LDS, held in registers in between:
+// rows behind the sequence's end read as zeros (buffer loads past num_records).
+template <int PPR>
+struct Tile {
+  static constexpr int kPieces = 64 * PPR / 256;
+  u32x4 x[kPieces];
+  // base: the chunk's first row; pitch: bytes between rows; left: rows of the sequence
+  __device__ __forceinline__ void load(const unsigned char* base, uint32_t pitch, int left, int tid) {
+    const int rows = left < 64 ? left : 64;
+    const uint32_t bytes = static_cast<uint32_t>(rows - 1) * pitch + PPR * 16;
+    __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<unsigned char*>(base), 0, bytes, 0x00020000);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = tid + 256 * i;
+      const int off = static_cast<int>(static_cast<uint32_t>(at / PPR) * pitch + (at % PPR) * 16);
+      x[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+    }
+  }
+  __device__ __forceinline__ void store(unsigned char* tile, int tid) const {
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+      const int at = tid + 256 * i;
+      *reinterpret_cast<u32x4*>(tile + 16 * piece_at<PPR>(at / PPR, at % PPR)) = x[i];
+    }
+  }
+};
+
+// What a workgroup works on: false where it has nothing to do.
+struct LinTask {
+  int64_t tok0;     // first token row of the segment
+  int64_t len;      // tokens of the segment
+  int64_t n;        // sequence
+  int64_t slot;     // scan slot
+  int h, vblk;
+  bool first, last; // segment of its sequence
+};
+
+__device__ __forceinline__ bool find_task(const LinParams& p, LinTask& t) {
+  const int sub = p.heads_per_task * p.vblocks;
+  const int64_t b = blockIdx.x;
+  const int64_t i = b >> 3;
+  const int64_t task = (i / sub) * 8 + (b & 7);
+  if (task >= p.tasks) return false;
+  const int s = static_cast<int>(i % sub);
+  const int groups = p.H / p.heads_per_task;
+  const int64_t w = task / groups;
+  t.h = static_cast<int>(task % groups) * p.heads_per_task + s / p.vblocks;
+  t.vblk = s % p.vblocks;
+  t.slot = w;
+  int64_t begin, end, seg;
+  if (p.cu_seqlens) {
+    // the last n with cu[n] / seg_len + n <= w, 64 candidates at a time
+    const int lane = threadIdx.x & 63;
+    int64_t lo = 0, size = p.N;
+    while (size > 1) {
+      const int64_t step = (size + 63) / 64;
+      const int64_t at = lo + lane * step;
+      const bool ok = lane * step < size && p.cu_seqlens[at] / p.seg_len + at <= w;
+      const int c = __popcll(__ballot(ok));
+      const int64_t skip = (c > 0 ? c - 1 : 0) * step;
+      lo += skip;
+      size = size - skip < step ? size - skip : step;
+    }
+    t.n = lo;
+    begin = p.cu_seqlens[lo];
+    end = p.cu_seqlens[lo + 1];
+    seg = w - (begin / p.seg_len + lo);
+  } else {
+    t.n = w / p.segs_per_seq;
+    seg = w - t.n * p.segs_per_seq;
+    begin = t.n * p.T;
+    end = begin + p.T;
+  }
+  const int64_t total = end - begin;
+  const int64_t at = seg * p.seg_len;
+  t.first = seg == 0;
+  if (seg < 0 || (seg > 0 && at >= total)) return false;
+  t.tok0 = begin + at;
+  t.len = total - at < p.seg_len ? total - at : p.seg_len;
+  t.last = at + t.len >= total;
+  return true;
+}
+
+// Element offset of token row r (n * T + t, or a packed row) in a strided input.
+__device__ __forceinline__ int64_t row_offset(const LinParams& p, const int64_t (&st)[3], int64_t n,
+                                              int64_t row) {
+  if (p.cu_seqlens) return row * st[1];
+  return n * st[0] + (row - n * p.T) * st[1];
+}
+
+// S[t][c]: keys 32 (t / 2) + 8 grp + 4 (t % 2) + j of the value row of column m.
+template <int KT, int NC>
+__device__ __forceinline__ void load_state(f32x4 (&S)[KT][NC], const void* base, int64_t at, bool bf16,
+                                           int K, int row0, int grp, int m) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t row = at + static_cast<int64_t>(row0 + 4 * NC * (m >> 2) + 4 * c + (m & 3)) * K;
+#pragma unroll
+    for (int t = 0; t < KT; t += 2) {
+      float x[8];
+      if (bf16) load8<true>(base, row + 16 * t + 8 * grp, x);
+      else load8<false>(base, row + 16 * t + 8 * grp, x);
+      S[t][c] = f32x4{x[0], x[1], x[2], x[3]};
+      S[t + 1][c] = f32x4{x[4], x[5], x[6], x[7]};
+    }
+  }
+}
+
+template <int KT, int NC>
+__device__ __forceinline__ void store_state(const f32x4 (&S)[KT][NC], void* base, int64_t at, bool bf16,
+                                            int K, int row0, int grp, int m) {
+#pragma unroll
+  for (int c = 0; c < NC; ++c) {
+    const int64_t row = at + static_cast<int64_t>(row0 + 4 * NC * (m >> 2) + 4 * c + (m & 3)) * K;
+#pragma unroll
+    for (int t = 0; t < KT; t += 2) {
+      const int64_t idx = row + 16 * t + 8 * grp;
+      if (bf16) {
+        *reinterpret_cast<bf16x8*>(static_cast<unsigned short*>(base) + idx) = pack8(S[t][c], S[t + 1][c]);
+      } else {
+        f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(base) + idx);
+        q[0] = S[t][c];
+        q[1] = S[t + 1][c];
+      }
+    }
+  }
+}
+
+// S <- D S + K^T (V w) for one chunk; vf: the wave's V operands.
+template <bool BF16, int KD, int NC, bool LOW>
+__device__ __forceinline__ void update_state(f32x4 (&S)[KD / 16][NC],
+                                             const typename FragOf<BF16>::type (&vf)[NC][2],
+                                             const unsigned char* k_tile, const Gates& gt, int grp,
+                                             int m) {
+  typedef typename FragOf<BF16>::type Frag;
+  constexpr int kPpr = KD * (BF16 ? 2 : 4) / 16;
+  Frag vw[NC][2], vl[NC][2];
+#pragma unroll
+  for (int kb = 0; kb < 2; ++kb) {
+    const f32x4 wlo = *reinterpret_cast<const f32x4*>(&gt.w[32 * kb + 4 * grp]);
+    const f32x4 whi = *reinterpret_cast<const f32x4*>(&gt.w[32 * kb + 16 + 4 * grp]);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) scale_frag<LOW>(vf[c][kb], wlo, whi, vw[c][kb], vl[c][kb]);
+  }
+  const float D = gt.D;
+#pragma unroll
+  for (int t = 0; t < KD / 16; ++t) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) S[t][c] *= D;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      Frag kf;
+      col_frag<kPpr>(k_tile, 32 * (t / 2) + 4 * (t % 2), 8, kb, grp, m, kf);
+#pragma unroll
+      for (int c = 0; c < NC; ++c) {
+        S[t][c] = mma(kf, vw[c][kb], S[t][c]);
+        if constexpr (LOW) S[t][c] = mma(kf, vl[c][kb], S[t][c]);
+      }
+    }
+  }
+}
+
+}  // namespace kda

@@ -1,0 +1,206 @@
+"""Linear attention with one decay per head: binding of kda_linear (include/kda.h)."""
+
+import ctypes
+
+from . import KdaError, _raise_if, kda_last_error, load_library
+from ._tensors import dtype_code, is_tensor, need, on_device, run_on, steps
+
+__all__ = ["kda_linear", "kda_linear_args", "kda_linear_check", "kda_linear_plan",
+           "kda_linear_workspace_bytes", "make_linear_args"]
+
+_P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+
+
+class kda_linear_args(ctypes.Structure):
+    _fields_ = (
+        [(n, _P) for n in ("q", "k", "v", "g", "log_decay", "state_in", "cu_seqlens", "o",
+                           "state_out", "workspace")]
+        + [("workspace_bytes", ctypes.c_size_t)]
+        + [(n, _I64) for n in ("B", "T", "H", "Hk", "K", "V", "N")]
+        + [(f"{x}_stride_{d}", _I64) for x in "qkv" for d in ("batch", "token", "head")]
+        + [(n, _I32) for n in ("io_dtype", "state_dtype", "g_dtype")]
+        + [("scale", ctypes.c_float), ("segment_tokens", _I64), ("ssm_state_indices", _P),
+           ("state_out_indices", _P), ("state_pool_slots", _I64), ("state_slot_pitch", _I64)])
+
+
+class kda_linear_plan_info(ctypes.Structure):
+    _fields_ = [("decode", _I32), ("value_block", _I32), ("segment_tokens", _I64),
+                ("segments_bound", _I64), ("workgroups", _I64), ("state_workgroups", _I64),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+def _ptr(x):
+    return x if x is None or isinstance(x, int) else x.data_ptr()
+
+
+def make_linear_args(*, B, T, H, N, Hk=None, K=128, V=128, io_dtype=0, state_dtype=0,
+                     g_dtype=1, q_stride=None, k_stride=None, v_stride=None, **kw):
+    """Fill a kda_linear_args from raw pointers (ints), tensors or None; strides default to
+    contiguous tensors."""
+    Hk = H if Hk is None else Hk
+    a = kda_linear_args()
+    a.B, a.T, a.H, a.Hk, a.K, a.V, a.N = B, T, H, Hk, K, V, N
+    a.io_dtype, a.state_dtype, a.g_dtype = io_dtype, state_dtype, g_dtype
+    for x, st, heads, dim in (("q", q_stride, Hk, K), ("k", k_stride, Hk, K),
+                              ("v", v_stride, H, V)):
+        for d, s in zip(("batch", "token", "head"), st or (T * heads * dim, heads * dim, dim)):
+            setattr(a, f"{x}_stride_{d}", s)
+    for name, x in kw.items():
+        if name in ("scale", "segment_tokens", "workspace_bytes", "state_pool_slots",
+                    "state_slot_pitch"):
+            setattr(a, name, x)
+        else:
+            setattr(a, name, _ptr(x))
+    return a
+
+
+def kda_linear_workspace_bytes(args):
+    n = ctypes.c_size_t(0)
+    _raise_if(load_library().kda_linear_workspace_bytes(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def kda_linear_check(args):
+    """Host-only validation; returns the status code (0 = OK)."""
+    return load_library().kda_linear_check(ctypes.byref(args))
+
+
+def kda_linear_plan(args):
+    info = kda_linear_plan_info()
+    _raise_if(load_library().kda_linear_plan(ctypes.byref(args), ctypes.byref(info)))
+    return {f: getattr(info, f) for f, _ in kda_linear_plan_info._fields_}
+
+
+def _state_shape(t, name, shape, dtype):
+    need(tuple(t.shape) == shape, 2, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    need(t.dtype == dtype, 3, f"{name} is {t.dtype}, the state dtype is {dtype}")
+
+
+def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=None, scale=None,
+               output_final_state=True, state_dtype=None, o=None, state_out=None,
+               workspace=None, segment_tokens=0, ssm_state_indices=None,
+               state_out_indices=None, stream=None):
+    """Linear attention with one decay per head, forward, on the current (or given) stream:
+
+        S <- exp(g_t + log_decay) S + v_t k_t^T ;  o_t = scale * S q_t
+
+    q, k: [B, T, Hk, K] (K 64 or 128), v: [B, T, H, V] (V a multiple of 64 up to 512), bf16
+    or fp32 CUDA tensors; Hk divides H and head h reads q/k head h // (H // Hk). Only their
+    last axis has to be contiguous (the other strides multiples of 8), so slices of one
+    projection are taken as they are. g: [B, T, H] log decays (<= 0; -inf empties the
+    state) of q's dtype or fp32, or None. log_decay: fp32 [H], a fixed decay of each head,
+    or None; where both are given they add.
+    state_in: [N, H, V, K] or None (zeros); state_out=state_in updates in place.
+    cu_seqlens: int64 [N + 1] (B = 1) or None.
+    1 <= T <= 8 in the fixed layout is the step of single (or a few draft) tokens: each state
+    is read and written once. segment_tokens: 0 automatic, negative serial, positive the
+    time-segment length (a multiple of 64).
+    ssm_state_indices (int32 [N]): state_in is a pool [slots, H, V, K] (its first axis may
+    be padded), sequence n starts from slot ssm_state_indices[n] and writes its final state
+    to slot state_out_indices[n] (None: the slot it read); the returned state is the pool.
+    Ids outside the pool start from zero and write nothing.
+    Returns (o, state_out or None).
+    """
+    import torch
+
+    is_tensor(q, "q")
+    is_tensor(k, "k")
+    is_tensor(v, "v")
+    need(q.dim() == 4 and v.dim() == 4, 2, "q and v must have four axes, [B, T, heads, dim]")
+    B, T, Hk, K = q.shape
+    H, V = v.shape[2:]
+    io = dtype_code(q, "q")
+    dt = q.dtype
+    need(k.shape == q.shape, 2, f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
+    need(v.shape[:2] == q.shape[:2], 2, f"v has shape {tuple(v.shape)}, expected "
+         f"({B}, {T}, heads, dim)")
+    need(k.dtype == dt and v.dtype == dt, 3, f"q, k, v are {dt}, {k.dtype}, {v.dtype}")
+    need(Hk >= 1 and H >= 1 and H % Hk == 0, 2, f"{Hk} q/k heads do not divide {H} heads")
+    sq, sk, sv = steps(q), steps(k), steps(v)
+    need(T == 0 or B == 0 or (sq[3] == 1 and sk[3] == 1 and sv[3] == 1), 2,
+         "the last axis of q, k and v must be contiguous")
+    N = B
+    if cu_seqlens is not None:
+        is_tensor(cu_seqlens, "cu_seqlens", torch.int64)
+        need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, 2,
+             "cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
+        need(cu_seqlens.is_contiguous(), 2, "cu_seqlens must be contiguous")
+        need(B == 1, 2, f"packed varlen needs B = 1 (got {B})")
+        N = cu_seqlens.numel() - 1
+    gt = 1
+    if g is not None:
+        is_tensor(g, "g")
+        gt = dtype_code(g, "g")
+        need(gt == 1 or gt == io, 3, f"g is {g.dtype}, expected {dt} or float32")
+        need(tuple(g.shape) == (B, T, H), 2, f"g has shape {tuple(g.shape)}, expected "
+             f"{(B, T, H)}")
+        need(g.is_contiguous(), 2, "g must be contiguous")
+    if log_decay is not None:
+        is_tensor(log_decay, "log_decay", torch.float32)
+        need(tuple(log_decay.shape) == (H,) and log_decay.is_contiguous(), 2,
+             f"log_decay must be a contiguous [{H}]")
+    if state_dtype is None:
+        state_dtype = state_in.dtype if state_in is not None else dt
+    need(state_dtype in (torch.bfloat16, torch.float32), 3, f"state dtype {state_dtype}")
+    slots = pitch = 0
+    if ssm_state_indices is not None:
+        need(state_in is not None, 10, "a state pool needs state_in")
+        need(state_in.dim() == 4 and state_in.shape[0] >= 1, 2,
+             "a state pool needs state_in [slots, H, V, K]")
+        slots = state_in.shape[0]
+        _state_shape(state_in, "the state pool", (slots, H, V, K), state_dtype)
+        st = state_in.stride()
+        need(st[3] == 1 and st[2] == K and (H == 1 or st[1] == V * K), 2,
+             "each state pool slot must be contiguous")
+        pitch = st[0] if slots > 1 else H * V * K
+        need(pitch % 8 == 0, 2, "the state pool's slot pitch must be a multiple of 8 elements")
+        need(state_out is None or state_out is state_in
+             or state_out.data_ptr() == state_in.data_ptr(), 6,
+             "with a state pool, state_out must be None or state_in")
+        state_out = state_in
+        for name, ids in (("ssm_state_indices", ssm_state_indices),
+                          ("state_out_indices", state_out_indices)):
+            if ids is not None:
+                is_tensor(ids, name, torch.int32)
+                need(tuple(ids.shape) == (N,) and ids.is_contiguous(), 2,
+                     f"{name} must be a contiguous [{N}]")
+    else:
+        need(state_out_indices is None, 10, "state_out_indices needs ssm_state_indices")
+        if state_in is not None:
+            _state_shape(state_in, "state_in", (N, H, V, K), state_dtype)
+            need(state_in.is_contiguous(), 2, "state_in must be contiguous")
+        if state_out is not None:
+            _state_shape(state_out, "state_out", (N, H, V, K), state_dtype)
+            need(state_out.is_contiguous(), 2, "state_out must be contiguous")
+    if o is not None:
+        need(o.shape == v.shape and o.dtype == dt and o.is_contiguous(), 2,
+             f"o must be a contiguous {tuple(v.shape)} of {dt}")
+    if workspace is not None:
+        need(workspace.is_contiguous(), 2, "workspace must be contiguous")
+    dev = q.device
+    on_device(dev, q=q, k=k, v=v, g=g, log_decay=log_decay, state_in=state_in,
+              cu_seqlens=cu_seqlens, o=o, state_out=state_out, workspace=workspace,
+              ssm_state_indices=ssm_state_indices, state_out_indices=state_out_indices)
+    lib = load_library()
+    with run_on(dev, stream) as handle:
+        if o is None:
+            o = torch.empty((B, T, H, V), dtype=dt, device=dev)
+        if state_out is None and output_final_state:
+            state_out = torch.empty((N, H, V, K), dtype=state_dtype, device=dev)
+        a = kda_linear_args(
+            q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(log_decay), _ptr(state_in),
+            _ptr(cu_seqlens), o.data_ptr(), _ptr(state_out), None, 0, B, T, H, Hk, K, V, N,
+            sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], io,
+            0 if state_dtype == torch.bfloat16 else 1, gt, 0.0 if scale is None else scale,
+            segment_tokens, _ptr(ssm_state_indices), _ptr(state_out_indices), slots, pitch)
+        if workspace is None:
+            size = kda_linear_workspace_bytes(a)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        if workspace is not None:
+            a.workspace = workspace.data_ptr()
+            a.workspace_bytes = workspace.numel() * workspace.element_size()
+        status = lib.kda_linear(ctypes.byref(a), handle)
+    if status:
+        raise KdaError(status, kda_last_error())
+    return o, state_out

@@ -371,6 +371,177 @@ typedef struct kda_plan_info {
 } kda_plan_info;
 kda_status kda_prefill_plan(const kda_prefill_args *a, int32_t num_cus, kda_plan_info *out);
 
+/* ------------------------------------------------------------------------------------
+ * Linear attention with one decay per head
+ *
+ * For every sequence n and head h, starting from the state S (V x K) in state_in[n, h]
+ * (or zeros), every token t updates
+ *
+ *     S <- exp(g_t[h] + log_decay[h]) S + v_t k_t^T ;  o_t = scale * S q_t
+ *
+ * and the final S is written to state_out[n, h]: the same state layout, pool and packed
+ * varlen contract as kda_prefill, for the layers whose decay is one number per head and
+ * whose write is a plain outer product. Chunks of 64 tokens are evaluated as matrix
+ * products; 1 <= T <= 8 tokens in the fixed layout (automatic geometry) run the token
+ * loop (one read and one write of each state, no workspace).
+ *
+ * The log decays are meant to be <= 0; -inf is allowed (it empties the state before the
+ * token's own write). A NaN or infinity in v reaches the outputs of its whole 64-token
+ * chunk, as in any product with a causal mask of zeros; other sequences and heads are
+ * never touched by it.
+ */
+typedef struct kda_linear_args {
+  /* Inputs (device, read only). q, k: [B, T, Hk, K], v: [B, T, H, V] of io_dtype, the
+     last axis contiguous, the others by the strides below; head h reads q/k head
+     h / (H / Hk). g: contiguous [B, T, H] of g_dtype, or NULL (0). log_decay: FP32 [H],
+     or NULL (0). */
+  const void *q, *k, *v, *g;
+  const float *log_decay;
+  /* [N, H, V, K] of state_dtype, or NULL for a zero initial state. */
+  const void *state_in;
+  /* int64 [N + 1] packed-varlen offsets (B must be 1), or NULL; as in kda_prefill_args. */
+  const int64_t *cu_seqlens;
+
+  /* Outputs (device). o: contiguous [B, T, H, V] of io_dtype, must not overlap any input.
+     state_out: [N, H, V, K] of state_dtype, or NULL; may be exactly state_in. */
+  void *o;
+  void *state_out;
+
+  /* Caller-owned scratch of kda_linear_workspace_bytes() bytes, 256-byte aligned; may be
+     NULL when that is 0. Nothing in it needs clearing; two calls that overlap in time
+     (also as replays of two captured graphs) need one each. */
+  void *workspace;
+  size_t workspace_bytes;
+
+  int64_t B, T, H, Hk, K, V, N; /* Hk divides H; K is 64 or 128; V a multiple of 64 up
+                                   to 512; N = number of sequences */
+  /* Strides in elements: batch, token, head. Not negative, multiples of 8 (0 repeats a
+     row), a token stride of at most 2^22. */
+  int64_t q_stride[3], k_stride[3], v_stride[3];
+  int32_t io_dtype;    /* kda_dtype of q, k, v and o. FP32 is computed in FP32 throughout;
+                          BF16 uses BF16 matrix products with FP32 sums and states */
+  int32_t state_dtype; /* kda_dtype of state_in and state_out */
+  int32_t g_dtype;     /* kda_dtype of g */
+  float scale;         /* output scale s; 0 selects 1/sqrt(K) */
+
+  /* Time segments: tokens per segment (a positive multiple of 64), 0 = automatic,
+     negative = one serial run per sequence. With segments, the end state of each later
+     segment from zero is formed first (in parallel), the start states follow by an
+     elementwise scan, and all segments' outputs then run in parallel: half as many bytes
+     again for a path of one segment's length. Results differ from the serial form only
+     by rounding. */
+  int64_t segment_tokens;
+
+  /* State pool: as in kda_prefill_args (state_in is the pool, updated in place), with
+     separate slots for reading and writing: sequence n starts from slot
+     ssm_state_indices[n] and writes slot state_out_indices[n] (NULL: the slot it read).
+     Several sequences may read one slot (a shared prefix); slots written must be
+     distinct and, unless it is the same sequence's, not read by the call (caller
+     contract, not checked). An id outside [0, state_pool_slots) starts from zero or
+     writes nothing. */
+  const int32_t *ssm_state_indices;
+  const int32_t *state_out_indices;
+  int64_t state_pool_slots;
+  int64_t state_slot_pitch; /* elements between slots (0 = H * V * K); a multiple of 8 */
+} kda_linear_args;
+
+typedef struct kda_linear_plan_info {
+  int32_t decode;             /* 1: the token loop */
+  int32_t value_block;        /* state rows (values) per workgroup */
+  int64_t segment_tokens;     /* 0: serial form */
+  int64_t segments_bound;     /* scan slots per head (bound on the number of segments) */
+  int64_t workgroups;         /* of the launch that writes o */
+  int64_t state_workgroups;   /* of the segments' state launch (0 in the serial form) */
+  size_t workspace_bytes;
+} kda_linear_plan_info;
+
+/* Host only, no HIP call: sizes and geometry / every check kda_linear does. */
+kda_status kda_linear_workspace_bytes(const kda_linear_args *a, size_t *bytes);
+kda_status kda_linear_check(const kda_linear_args *a);
+kda_status kda_linear_plan(const kda_linear_args *a, kda_linear_plan_info *out);
+/* Enqueue on `stream` (a hipStream_t of the current device). Asynchronous, allocates
+   nothing, may be captured. */
+kda_status kda_linear(const kda_linear_args *a, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Slots of a state pool
+ *
+ * A pool is [layers][slots][slot_elems]: slots slot_pitch elements apart, layers
+ * layer_pitch elements apart. slot_elems and both pitches are multiples of 8, bases
+ * 16-byte aligned.
+ */
+typedef struct kda_pool {
+  void *base;
+  int64_t slots, layers, slot_elems, slot_pitch, layer_pitch;
+  int32_t dtype; /* kda_dtype */
+} kda_pool;
+
+/* dst[l][dst_idx[i]] <- src[l][src_idx[i]] for every layer l and pair i (int32 [pairs]
+   device arrays): copies, forks (one source in many pairs), restores from another pool or
+   a checkpoint buffer (also of the other dtype: FP32 -> BF16 rounds to nearest even), and
+   clears: a source id outside [0, src->slots) writes zeros. A destination id outside
+   [0, dst->slots) writes nothing. src and dst may be the same pool; a destination must
+   not appear twice nor be another pair's source (caller contract, not checked); a pair
+   with src_idx == dst_idx within one pool leaves its slot as it is. */
+typedef struct kda_pool_copy_args {
+  kda_pool src, dst; /* equal layers and slot_elems */
+  const int32_t *src_idx, *dst_idx;
+  int64_t pairs;
+} kda_pool_copy_args;
+kda_status kda_pool_copy_check(const kda_pool_copy_args *a);
+kda_status kda_pool_copy(const kda_pool_copy_args *a, void *stream);
+
+/* Compaction: moves as few slots as possible so that the live ones are the first ones.
+   idx: int32 [n] device, the slots in use (ids outside [0, slots) are ignored and handed
+   through; an id may appear more than once). With L distinct live slots, the k-th live
+   slot >= L (ascending) is copied to the k-th free slot < L; the others stay, and slots
+   from L on keep their contents. new_idx[i] (may be idx) is the slot that idx[i] has
+   afterwards, *count (device int32) is L. slots is at most KDA_POOL_COMPACT_SLOTS.
+   workspace: kda_pool_compact_workspace_bytes() bytes, 256-byte aligned. */
+#define KDA_POOL_COMPACT_SLOTS (1 << 18)
+typedef struct kda_pool_compact_args {
+  kda_pool pool;
+  const int32_t *idx;
+  int32_t *new_idx;
+  int32_t *count;
+  int64_t n;
+  void *workspace;
+  size_t workspace_bytes;
+} kda_pool_compact_args;
+kda_status kda_pool_compact_workspace_bytes(const kda_pool_compact_args *a, size_t *bytes);
+kda_status kda_pool_compact_check(const kda_pool_compact_args *a);
+kda_status kda_pool_compact(const kda_pool_compact_args *a, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Gated norm: what follows the attention's output, or stands between two blocks
+ *
+ *     y = residual + scale * act(gate) * weight * x / sqrt(mean(x^2) + eps)
+ *     z = next_weight * y / sqrt(mean(y^2) + eps)
+ *
+ * over rows of D elements, in FP32, each result rounded once (z from the unrounded y).
+ * gate, weight and residual may be NULL (1, 1 and 0); z is written when next_out is set
+ * (next_weight NULL: 1).
+ */
+typedef enum kda_act { KDA_ACT_SIGMOID = 0, KDA_ACT_SILU = 1 } kda_act;
+
+typedef struct kda_gated_norm_args {
+  /* [M, G, D] of io_dtype, strides in elements for M and G (not negative, multiples of
+     8), D contiguous. */
+  const void *x, *gate, *residual;
+  const float *weight, *next_weight; /* FP32 [D] */
+  /* Contiguous [M, G, D] of io_dtype. out may be exactly x, gate or residual where that
+     is contiguous; otherwise the outputs overlap no input and not each other. */
+  void *out, *next_out;
+  int64_t M, G, D; /* D a multiple of 8 up to 16384 */
+  int64_t x_stride[2], gate_stride[2], residual_stride[2];
+  int32_t io_dtype;
+  int32_t act; /* kda_act of the gate */
+  float eps;   /* >= 0 */
+  float scale;
+} kda_gated_norm_args;
+kda_status kda_gated_norm_check(const kda_gated_norm_args *a);
+kda_status kda_gated_norm(const kda_gated_norm_args *a, void *stream);
+
 int32_t kda_abi_version(void);
 
 #ifdef __cplusplus

@@ -25,6 +25,7 @@ Modules
 ``transforms``  in-kernel q/k L2 norm, beta-from-logit and the lower-bounded gate.
                 The gate formula is not printed on the pages: parity unpinned against
                 the pages for ``safe_gate`` (only its range and special case are pinned).
+``linear``      linear attention with one decay per head, pool compaction, gated norm.
 """
 
 from .kda_token import checkpoint_starts, kda_recurrence_fp64, token_step
@@ -35,6 +36,7 @@ from .kda_chunk import (
     inverse_forward_substitution,
     inverse_neumann,
 )
+from .linear import compact_slots, gated_norm_fp64, linear_recurrence_fp64
 from .transforms import l2_normalize, sigmoid, safe_gate
 
 __all__ = [
@@ -49,4 +51,7 @@ __all__ = [
     "l2_normalize",
     "sigmoid",
     "safe_gate",
+    "linear_recurrence_fp64",
+    "compact_slots",
+    "gated_norm_fp64",
 ]
