@@ -16,14 +16,14 @@
 //   P^T tile (j, i)     = K . Q^T, scaled by its decays, through LDS to all waves
 //   O^T tile (value, i) = S^T Q^T (scaled by s exp(G_i)) + V^T P^T
 //   S tile (key, value) = exp(G_C) S + K^T (V exp(G_C - G_j))
-// Two 16-key accumulator tiles side by side hold keys 8 grp .. 8 grp + 7 of 32 in each
-// lane (the K^T operand's rows are permuted so), which is the operand order of a plain
-// 16-byte read of Q. For the contractions over tokens both sides use the order
+// Two 16-key accumulator tiles hold keys 8 grp .. 8 grp + 7 of 32 in each lane (the K^T
+// operand's rows are permuted so), which are those of a plain 16-byte read of Q. For the contractions over tokens both sides use the order
 // kappa(kb, grp, e) = 32 kb + 16 (e / 4) + 4 grp + e % 4.
 //
-// LDS tiles are rows of 16-byte pieces, piece p of row r stored at p ^ (r % 16) (8-piece
-// rows: p ^ (r / 2 % 8)), so that the 16 rows an operand read touches lie in different
-// banks. BF16 operands that need eight tokens of one column come from the transposing LDS
+// LDS tiles are rows of 16-byte pieces, permuted within a row by an exclusive or with a
+// number of the row's: one that differs over the 16 rows of a plain operand read, and in
+// its upper bits over the four rows from which 16 lanes of a transposing read take 32 or
+// 64 bytes each, so that both touch every bank alike. BF16 operands that need eight tokens of one column come from the transposing LDS
 // read; FP32 ones (FP32 I/O) from 4-byte reads.
 #pragma once
 
@@ -55,14 +55,20 @@ __device__ __forceinline__ f32x4 mma(const F32x8& a, const F32x8& b, f32x4 c) {
   return c;
 }
 
+// Piece p of row r of a tile is stored at p ^ piece_swap(r).
+template <int PPR>
+__device__ __forceinline__ int piece_swap(int r) {
+  static_assert(PPR == 8 || PPR == 16 || PPR == 32, "row sizes of 128, 256 or 512 bytes");
+  const int q = (r >> 2) & 3, low = (((q ^ (q >> 1)) & 1) << 1) | (q >> 1);  // 0, 2, 3, 1
+  return (PPR >= 16 ? (r & 3) << 2 : (r & 2) << 1) | low;
+}
 __device__ __forceinline__ void to_frag(f32x4 lo, f32x4 hi, bf16x8& f) { f = pack8(lo, hi); }
 __device__ __forceinline__ void to_frag(f32x4 lo, f32x4 hi, F32x8& f) { f = F32x8{lo, hi}; }
 
 // Index (in 16-byte pieces) of piece p of row r in a tile of PPR pieces per row.
 template <int PPR>
 __device__ __forceinline__ int piece_at(int r, int p) {
-  static_assert(PPR == 8 || PPR == 16 || PPR == 32, "row sizes of 128, 256 or 512 bytes");
-  return r * PPR + (p ^ (PPR >= 16 ? (r & 15) : ((r >> 1) & 7)));
+  return r * PPR + (p ^ piece_swap<PPR>(r));
 }
 
 // Operand of row `row` (this lane's token) and its eight keys 32 kb + 8 grp ...
@@ -132,53 +138,100 @@ __device__ __forceinline__ void scale_frag(const F32x8& x, f32x4 wlo, f32x4 whi,
   f.hi = x.hi * whi;
 }
 
-// The decay factors of one chunk, in LDS.
+// The decay factors of one chunk, in LDS, by its four 16-token blocks.
 struct Gates {
-  double G[kLinChunk];  // inclusive prefix sums of the log2 decays
-  float a[kLinChunk];   // s * decay from the start of the token's 16-token block to it
-  float b[kLinChunk];   // decay from the token to the end of its block
-  float w[kLinChunk];   // decay from the token to the end of the chunk (0 behind the end)
-  float d[kLinChunk];   // s * decay from the start of the chunk to the token
+  double L[kLinChunk];  // sums of the log2 decays from the start of the token's block to it
+  float a[kLinChunk];   // s * decay from the start of the block to the token
+  float b[kLinChunk];   // decay from the token to the end of the block; 0 behind the end
   float E[4];           // total decay of each block
-  float D;              // total decay of the chunk
 };
 
 constexpr double kLog2e = 1.4426950408889634074;
 
-// Log2 decay of token t of the chunk for head h; tok0 is the chunk's first token row.
-__device__ __forceinline__ double load_log_decay(const LinParams& p, int64_t tok0, int t, int left,
-                                                 int h) {
-  if (t >= left) return 0.0;
-  double x = 0.0;
-  if (p.g) {
-    const int64_t at = (tok0 + t) * p.H + h;
-    x = p.g_bf16 ? load1<true>(p.g, at) : load1<false>(p.g, at);
-  }
-  if (p.log_decay) x += static_cast<double>(p.log_decay[h]);
-  // -inf (an emptied state) as a finite number whose factor is 0; NaN stays
-  return (x < -1000.0 ? -1000.0 : x) * kLog2e;
+template <int CTRL>
+__device__ __forceinline__ double dpp_shift(double x) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  u32x2 r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r[i] = static_cast<unsigned>(__builtin_amdgcn_update_dpp(0, static_cast<int>(w[i]), CTRL, 0xF, 0xF, true));
+  return __builtin_bit_cast(double, r);
 }
 
-// One wave, lane t = token t.
-__device__ __forceinline__ void make_gates(Gates& gt, double x, int t, int left, float scale) {
-  double G = x;
+__device__ __forceinline__ double read_lane(double x, int lane) {
+  const u32x2 w = __builtin_bit_cast(u32x2, x);
+  u32x2 r;
 #pragma unroll
-  for (int s = 1; s < 64; s <<= 1) {
-    const double y = __shfl_up(G, s);
-    if (t >= s) G += y;
+  for (int i = 0; i < 2; ++i)
+    r[i] = static_cast<unsigned>(__builtin_amdgcn_readlane(static_cast<int>(w[i]), lane));
+  return __builtin_bit_cast(double, r);
+}
+
+__device__ __forceinline__ float exp2_of(double x) {
+  return __builtin_amdgcn_exp2f(static_cast<float>(x));
+}
+
+// The log decay of a token as it is in memory: the g of head h at token row `row`.
+__device__ __forceinline__ float load_log_decay(const LinParams& p, int64_t row, int h) {
+  if (!p.g) return 0.f;
+  const int64_t at = row * p.H + h;
+  return p.g_bf16 ? load1<true>(p.g, at) : load1<false>(p.g, at);
+}
+
+// One wave makes the factors of block `blk`: every row of 16 lanes holds its 16 tokens, x
+// their log decays, `held` whether the token exists. The prefix sums are FP64, so that
+// their differences are exact to FP32 whatever the decays before the two tokens are.
+struct BlockGates {
+  double L;
+  float a, b, e;
+  __device__ __forceinline__ void make(float x, float fixed, bool held, float scale) {
+    double y = static_cast<double>(x) + static_cast<double>(fixed);
+    // -inf (an emptied state) as a finite number whose factor is 0; NaN stays
+    y = (y < -1000.0 ? -1000.0 : y) * kLog2e;
+    y = held ? y : 0.0;
+    y += dpp_shift<0x111>(y);  // row_shr 1, 2, 4, 8
+    y += dpp_shift<0x112>(y);
+    y += dpp_shift<0x114>(y);
+    y += dpp_shift<0x118>(y);
+    const double total = read_lane(y, 15);
+    L = y;
+    a = scale * exp2_of(y);
+    b = held ? exp2_of(total - y) : 0.f;
+    e = exp2_of(total);
   }
-  const int blk = t & ~15;
-  const double before = __shfl(G, blk == 0 ? 0 : blk - 1);
-  const double start = blk == 0 ? 0.0 : before;
-  const double end = __shfl(G, blk + 15);
-  const double all = __shfl(G, 63);
-  gt.G[t] = G;
-  gt.a[t] = scale * __builtin_amdgcn_exp2f(static_cast<float>(G - start));
-  gt.b[t] = __builtin_amdgcn_exp2f(static_cast<float>(end - G));
-  gt.w[t] = t < left ? __builtin_amdgcn_exp2f(static_cast<float>(all - G)) : 0.f;
-  gt.d[t] = scale * __builtin_amdgcn_exp2f(static_cast<float>(G));
-  if ((t & 15) == 0) gt.E[t >> 4] = __builtin_amdgcn_exp2f(static_cast<float>(end - start));
-  if (t == 0) gt.D = __builtin_amdgcn_exp2f(static_cast<float>(all));
+  __device__ __forceinline__ void write(Gates& gt, int blk, int lane) const {
+    if (lane < 16) {
+      gt.L[16 * blk + lane] = L;
+      gt.a[16 * blk + lane] = a;
+      gt.b[16 * blk + lane] = b;
+      if (lane == 0) gt.E[blk] = e;
+    }
+  }
+};
+__device__ __forceinline__ void make_gates(Gates& gt, float x, float fixed, int blk, int lane, bool held,
+                                           float scale) {
+  BlockGates g;
+  g.make(x, fixed, held, scale);
+  g.write(gt, blk, lane);
+}
+
+// Decays of whole blocks of a chunk: before a block, behind it, and of all four.
+struct BlockDecays {
+  float before[4], behind[4], all;
+};
+__device__ __forceinline__ BlockDecays block_decays(const Gates& gt) {
+  const f32x4 E = *reinterpret_cast<const f32x4*>(gt.E);
+  BlockDecays r;
+  r.before[0] = 1.f;
+  r.before[1] = E[0];
+  r.before[2] = E[0] * E[1];
+  r.before[3] = r.before[2] * E[2];
+  r.behind[3] = 1.f;
+  r.behind[2] = E[3];
+  r.behind[1] = E[3] * E[2];
+  r.behind[0] = r.behind[1] * E[1];
+  r.all = r.before[3] * E[3];
+  return r;
 }
 
 // A tile of 64 rows x PPR pieces between memory and LDS, held in registers in between:
@@ -209,6 +262,54 @@ struct Tile {
   }
 };
 
+// A tile of 64 rows x PPR pieces from memory straight into LDS (asynchronous 16-byte loads,
+// one KB of consecutive LDS for each instruction of a wave), 64 PPR / 256 instructions per
+// wave. The lanes fetch the pieces in the order in which the tile stores them. Rows behind
+// the sequence's end repeat its last row: their keys and values meet a zero factor, their
+// queries' outputs are not stored.
+template <int PPR>
+struct AsyncTile {
+  static constexpr int kLoads = PPR / 4;  // instructions per wave
+  int off[kLoads];
+  static __device__ __forceinline__ int offset(int wave, int lane, int j, uint32_t pitch, int last) {
+    const int at = (wave * kLoads + j) * 64 + lane;
+    const int r = at / PPR;
+    const int piece = (at % PPR) ^ piece_swap<PPR>(r);
+    return static_cast<int>(static_cast<uint32_t>(r < last ? r : last) * pitch) + 16 * piece;
+  }
+  __device__ __forceinline__ void init(int wave, int lane, uint32_t pitch) {
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) off[j] = offset(wave, lane, j, pitch, 63);
+  }
+  // base: the chunk's first row; left: rows of the sequence from there on
+  __device__ __forceinline__ void load(const unsigned char* base, uint32_t pitch, int left,
+                                       unsigned char* tile, int wave, int lane) const {
+    typedef __attribute__((address_space(3))) void lds_void;
+    const int rows = left < 64 ? left : 64;
+    const uint32_t bytes = static_cast<uint32_t>(rows - 1) * pitch + PPR * 16;
+    __amdgpu_buffer_rsrc_t r = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<unsigned char*>(base), 0, bytes, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      const int o = rows == 64 ? off[j] : offset(wave, lane, j, pitch, rows - 1);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(tile + (wave * kLoads + j) * 1024), 16, o,
+                                               0, 0, 0);
+    }
+  }
+};
+
+// All but the `N` newest of the wave's memory operations are done (operations complete in
+// issue order), its LDS accesses too; then the workgroup's barrier. The tiles that every
+// wave has waited for are whole behind it.
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// The workgroup's barrier alone: the wave's LDS accesses are done, its memory operations may
+// be outstanding.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // What a workgroup works on: false where it has nothing to do.
 struct LinTask {
   int64_t tok0;     // first token row of the segment
@@ -232,7 +333,27 @@ __device__ __forceinline__ bool find_task(const LinParams& p, LinTask& t) {
   t.vblk = s % p.vblocks;
   t.slot = w;
   int64_t begin, end, seg;
-  if (p.cu_seqlens) {
+  if (p.longest_first) {
+    // one lane per sequence (at most 64): w is its rank by decreasing length
+    const int lane = threadIdx.x & 63, N = static_cast<int>(p.N);
+    int64_t from = 0, len = -1;
+    if (lane < N) {
+      from = p.cu_seqlens[lane];
+      len = p.cu_seqlens[lane + 1] - from;
+    }
+    const int chunks = static_cast<int>((len + 63) >> 6);
+    int rank = 0;
+    for (int j = 0; j < N; ++j) {
+      const int other = __builtin_amdgcn_readlane(chunks, j);
+      rank += other > chunks || (other == chunks && j < lane);
+    }
+    const uint64_t mine = __ballot(lane < N && rank == static_cast<int>(w));
+    const int n = __builtin_ctzll(mine);
+    t.n = n;
+    begin = p.cu_seqlens[n];
+    end = p.cu_seqlens[n + 1];
+    seg = 0;
+  } else if (p.cu_seqlens) {
     // the last n with cu[n] / seg_len + n <= w, 64 candidates at a time
     const int lane = threadIdx.x & 63;
     int64_t lo = 0, size = p.N;
@@ -299,38 +420,50 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[KT][NC], void* base
 #pragma unroll
     for (int t = 0; t < KT; t += 2) {
       const int64_t idx = row + 16 * t + 8 * grp;
+      const f32x4 x = S[t][c], y = S[t + 1][c];
       if (bf16) {
-        *reinterpret_cast<bf16x8*>(static_cast<unsigned short*>(base) + idx) = pack8(S[t][c], S[t + 1][c]);
+        *reinterpret_cast<bf16x8*>(static_cast<unsigned short*>(base) + idx) = pack8(x, y);
       } else {
         f32x4* q = reinterpret_cast<f32x4*>(static_cast<float*>(base) + idx);
-        q[0] = S[t][c];
-        q[1] = S[t + 1][c];
+        q[0] = x;
+        q[1] = y;
       }
     }
   }
 }
 
-// S <- D S + K^T (V w) for one chunk; vf: the wave's V operands.
+// The decays of a lane's tokens kappa(kb, grp, e) to the end of the chunk.
+struct KeyDecays {
+  f32x4 w[2][2];
+  __device__ __forceinline__ void read(const Gates& gt, const BlockDecays& bd, int grp) {
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        w[kb][i] = bd.behind[2 * kb + i] * *reinterpret_cast<const f32x4*>(&gt.b[32 * kb + 16 * i + 4 * grp]);
+  }
+};
+
+// S <- D S + K^T (V w) for one chunk; vf: the wave's V operands, w a token's decay to the
+// end of the chunk.
 template <bool BF16, int KD, int NC, bool LOW>
 __device__ __forceinline__ void update_state(f32x4 (&S)[KD / 16][NC],
                                              const typename FragOf<BF16>::type (&vf)[NC][2],
-                                             const unsigned char* k_tile, const Gates& gt, int grp,
-                                             int m) {
+                                             const unsigned char* k_tile, const Gates& gt,
+                                             const BlockDecays& bd, int grp, int m) {
   typedef typename FragOf<BF16>::type Frag;
   constexpr int kPpr = KD * (BF16 ? 2 : 4) / 16;
   Frag vw[NC][2], vl[NC][2];
+  KeyDecays kd;
+  kd.read(gt, bd, grp);
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb) {
-    const f32x4 wlo = *reinterpret_cast<const f32x4*>(&gt.w[32 * kb + 4 * grp]);
-    const f32x4 whi = *reinterpret_cast<const f32x4*>(&gt.w[32 * kb + 16 + 4 * grp]);
+  for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-    for (int c = 0; c < NC; ++c) scale_frag<LOW>(vf[c][kb], wlo, whi, vw[c][kb], vl[c][kb]);
-  }
-  const float D = gt.D;
+    for (int c = 0; c < NC; ++c) scale_frag<LOW>(vf[c][kb], kd.w[kb][0], kd.w[kb][1], vw[c][kb], vl[c][kb]);
 #pragma unroll
   for (int t = 0; t < KD / 16; ++t) {
 #pragma unroll
-    for (int c = 0; c < NC; ++c) S[t][c] *= D;
+    for (int c = 0; c < NC; ++c) S[t][c] *= bd.all;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
       Frag kf;

@@ -7,16 +7,14 @@ namespace kda {
 
 namespace {
 
-// Workgroup: R = 64 NC value rows of one (segment, head); Z_p to the segment's scan slot,
-// the segment's total decay to scan_d.
-template <bool BF16, int KD, int NC, bool LOW>
-__global__ __launch_bounds__(256) void linear_states_kernel(LinParams p) {
-  typedef typename FragOf<BF16>::type Frag;
-  constexpr int kEs = BF16 ? 2 : 4;
-  constexpr int R = 64 * NC;
-  constexpr int kPprK = KD * kEs / 16, kPprV = R * kEs / 16;
-  __shared__ __align__(16) unsigned char k_tile[64 * KD * kEs];
-  __shared__ __align__(16) unsigned char v_tile[64 * R * kEs];
+// FP32 I/O: 64 value rows of one (segment, head); Z_p to the segment's scan slot, the
+// segment's total decay to scan_d.
+template <int KD>
+__global__ __launch_bounds__(256, 2) void linear_states_f32_kernel(LinParams p) {
+  constexpr int R = kLinRows;
+  constexpr int kPprK = KD / 4, kPprV = R / 4;
+  __shared__ __align__(16) unsigned char k_tile[64 * KD * 4];
+  __shared__ __align__(16) unsigned char v_tile[64 * R * 4];
   __shared__ Gates gates;
 
   LinTask task;
@@ -24,29 +22,29 @@ __global__ __launch_bounds__(256) void linear_states_kernel(LinParams p) {
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
   const int grp = lane >> 4, m = lane & 15;
   const int hk = task.h / (p.H / p.Hk);
-  const int row0 = task.vblk * R + wave * 16 * NC;
+  const int row0 = task.vblk * R + wave * 16;
   const unsigned char* kp = static_cast<const unsigned char*>(p.k) +
-                            (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * kEs;
+                            (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * 4;
   const unsigned char* vp = static_cast<const unsigned char*>(p.v) +
-                            (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * kEs;
-  const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * kEs);
-  const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * kEs);
+                            (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * 4;
+  const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * 4);
+  const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * 4);
 
-  f32x4 S[KD / 16][NC];
+  f32x4 S[KD / 16][1];
 #pragma unroll
-  for (int t = 0; t < KD / 16; ++t)
-#pragma unroll
-    for (int c = 0; c < NC; ++c) S[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < KD / 16; ++t) S[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   float total = 1.f;
 
   Tile<kPprK> kt;
   Tile<kPprV> vt;
-  double x = 0.0;
+  const float fixed = p.log_decay ? p.log_decay[task.h] : 0.f;
+  float x = 0.f;
   auto fetch = [&](int64_t at) {
     const int left = static_cast<int>(task.len - at < 64 ? task.len - at : 64);
     kt.load(kp + at * kpitch, kpitch, left, tid);
     vt.load(vp + at * vpitch, vpitch, left, tid);
-    if (wave == 0) x = load_log_decay(p, task.tok0 + at, lane, left, task.h);
+    const int i = 16 * wave + m;
+    x = load_log_decay(p, task.tok0 + at + (i < left ? i : left - 1), task.h);
   };
   if (task.len > 0) fetch(0);
   for (int64_t at = 0; at < task.len; at += 64) {
@@ -54,20 +52,130 @@ __global__ __launch_bounds__(256) void linear_states_kernel(LinParams p) {
     __syncthreads();
     kt.store(k_tile, tid);
     vt.store(v_tile, tid);
-    if (wave == 0) make_gates(gates, x, lane, left, 1.f);
+    make_gates(gates, x, fixed, wave, lane, 16 * wave + m < left, 1.f);
     __syncthreads();
     if (at + 64 < task.len) fetch(at + 64);
-    Frag vf[NC][2];
+    F32x8 vf[1][2];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
-#pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-        col_frag<kPprV>(v_tile, wave * 16 * NC + 4 * c, 4 * NC, kb, grp, m, vf[c][kb]);
-    total *= gates.D;
-    update_state<BF16, KD, NC, LOW>(S, vf, k_tile, gates, grp, m);
+    for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[0][kb]);
+    const BlockDecays bd = block_decays(gates);
+    total *= bd.all;
+    update_state<false, KD, 1, false>(S, vf, k_tile, gates, bd, grp, m);
   }
   const int64_t slot = static_cast<int64_t>(task.h) * p.slots + task.slot;
   store_state(S, p.scan_s, slot * p.V * KD, false, KD, row0, grp, m);
+  if (tid == 0 && task.vblk == 0) p.scan_d[slot] = total;
+}
+
+// BF16 I/O: the same by eight waves as in the output launch (kda_linear_chunks.hip): four
+// load the tiles of chunk c + 2 into a ring of three and make the decay factors of chunk
+// c + 1, four update the state.
+constexpr int kStages = 3;
+
+template <int KD, bool LOW>
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 4))) void linear_states_kernel(LinParams p) {
+  constexpr int R = kLinRows;
+  constexpr int kPprK = KD / 8, kPprV = R / 8;
+  constexpr int kTileK = 128 * KD, kStage = kTileK + 128 * R;
+  constexpr int kLoads = AsyncTile<kPprK>::kLoads + AsyncTile<kPprV>::kLoads;
+  extern __shared__ __align__(1024) unsigned char lds[];
+  Gates* const gates = reinterpret_cast<Gates*>(lds + kStages * kStage);
+
+  LinTask task;
+  if (!find_task(p, task) || task.last) return;  // uniform
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
+  const int grp = lane >> 4, m = lane & 15;
+  const int chunks = static_cast<int>((task.len + 63) >> 6);  // a segment with a later one is whole
+  const int64_t slot = static_cast<int64_t>(task.h) * p.slots + task.slot;
+
+  if (__builtin_amdgcn_readfirstlane(tid >> 8) != 0) {
+    __builtin_amdgcn_s_setprio(2);
+    const int hk = task.h / (p.H / p.Hk);
+    const unsigned char* kp = static_cast<const unsigned char*>(p.k) +
+                              (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * 2;
+    const unsigned char* vp = static_cast<const unsigned char*>(p.v) +
+                              (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * 2;
+    const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * 2);
+    const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * 2);
+    AsyncTile<kPprK> kt;
+    AsyncTile<kPprV> vt;
+    kt.init(wave, lane, kpitch);
+    vt.init(wave, lane, vpitch);
+    auto fetch = [&](int stage) {
+      unsigned char* st = lds + stage * kStage;
+      kt.load(kp, kpitch, 64, st, wave, lane);
+      vt.load(vp, vpitch, 64, st + kTileK, wave, lane);
+      kp += static_cast<uint64_t>(kpitch) * 64;
+      vp += static_cast<uint64_t>(vpitch) * 64;
+    };
+    const float fixed = p.log_decay ? p.log_decay[task.h] : 0.f;
+    auto log_decay = [&](int chunk) {
+      return load_log_decay(p, task.tok0 + 64 * static_cast<int64_t>(chunk) + 16 * wave + m, task.h);
+    };
+    float x0 = log_decay(0), x1 = 0.f;
+    fetch(0);
+    if (chunks > 1) {
+      x1 = log_decay(1);
+      fetch(1);
+    }
+    make_gates(gates[0], x0, fixed, wave, lane, true, 1.f);
+    int stage = 0;
+    auto step = [&](int chunk, float x_next, float& x_load) {
+      if (chunk + 1 < chunks) wait_and_meet<kLoads>();
+      else wait_and_meet<0>();
+      if (chunk + 2 < chunks) {
+        x_load = log_decay(chunk + 2);
+        fetch(stage >= 1 ? stage - 1 : kStages - 1);
+      }
+      make_gates(gates[(chunk + 1) & 1], x_next, fixed, wave, lane, chunk + 1 < chunks, 1.f);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    };
+    for (int chunk = 0; chunk < chunks; chunk += 2) {
+      step(chunk, x1, x0);
+      if (chunk + 1 < chunks) step(chunk + 1, x0, x1);
+    }
+    return;
+  }
+
+  f32x4 S[KD / 16][1];
+#pragma unroll
+  for (int t = 0; t < KD / 16; ++t) S[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float total = 1.f;
+  int stage = 0;
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    meet();
+    const unsigned char* k_tile = lds + stage * kStage;
+    const unsigned char* v_tile = k_tile + kTileK;
+    const Gates& gt = gates[chunk & 1];
+    bf16x8 vf[1][2], kf[KD / 16][2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[0][kb]);
+    const BlockDecays bd = block_decays(gt);
+    KeyDecays kd;
+    kd.read(gt, bd, grp);
+    // all reads before the products: left alone, each is read right before its use
+#pragma unroll
+    for (int t = 0; t < KD / 16; ++t)
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) col_frag<kPprK>(k_tile, 32 * (t / 2) + 4 * (t % 2), 8, kb, grp, m, kf[t][kb]);
+    __builtin_amdgcn_sched_barrier(0);
+    total *= bd.all;
+    bf16x8 vw[2], vl[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) scale_frag<LOW>(vf[0][kb], kd.w[kb][0], kd.w[kb][1], vw[kb], vl[kb]);
+#pragma unroll
+    for (int t = 0; t < KD / 16; ++t) {
+      S[t][0] *= bd.all;
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        S[t][0] = mma(kf[t][kb], vw[kb], S[t][0]);
+        if constexpr (LOW) S[t][0] = mma(kf[t][kb], vl[kb], S[t][0]);
+      }
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  store_state(S, p.scan_s, slot * p.V * KD, false, KD, task.vblk * R + wave * 16, grp, m);
   if (tid == 0 && task.vblk == 0) p.scan_d[slot] = total;
 }
 
@@ -101,40 +209,64 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(LinParams p, int K) {
   const int64_t base = static_cast<int64_t>(h) * p.slots + first;
   f32x4* z = reinterpret_cast<f32x4*>(p.scan_s) + base * per + e;
   const float* d = p.scan_d + base;
-  for (int64_t i = 0; i + 1 < segs; ++i) {
-    const f32x4 zi = z[i * per];
-    z[i * per] = s;
-    s = s * d[i] + zi;
+  // Eight segments' loads before their stores: a chain of dependent loads would be a trip
+  // through the memory for each segment.
+  int64_t i = 0;
+  for (; i + 8 < segs; i += 8) {
+    f32x4 zi[8];
+    float di[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      zi[j] = z[(i + j) * per];
+      di[j] = d[i + j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      z[(i + j) * per] = s;
+      s = s * di[j] + zi[j];
+    }
   }
-  z[(segs - 1) * per] = s;
+  f32x4 zi[8];
+  float di[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const bool has = i + j + 1 < segs;
+    zi[j] = has ? z[(i + j) * per] : f32x4{0.f, 0.f, 0.f, 0.f};
+    di[j] = has ? d[i + j] : 0.f;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (i + j >= segs) break;
+    z[(i + j) * per] = s;
+    s = s * di[j] + zi[j];
+  }
 }
 
-template <bool BF16, int KD, int NC, bool LOW>
+int64_t grid_of(const LinParams& p) {
+  return (p.tasks + 7) / 8 * 8 * p.heads_per_task * p.vblocks;
+}
+
+template <int KD, bool LOW>
 hipError_t go(const LinParams& p, hipStream_t stream) {
-  const int64_t sub = static_cast<int64_t>(p.heads_per_task) * p.vblocks;
-  const int64_t wgs = (p.tasks + 7) / 8 * 8 * sub;
-  hipLaunchKernelGGL((linear_states_kernel<BF16, KD, NC, LOW>), dim3(static_cast<unsigned>(wgs)),
-                     dim3(256), 0, stream, p);
+  constexpr int kLds = kStages * 128 * (KD + kLinRows) + 2 * sizeof(Gates);
+  static_assert(kLds <= 80 * 1024, "two workgroups per compute unit");
+  hipLaunchKernelGGL((linear_states_kernel<KD, LOW>), dim3(static_cast<unsigned>(grid_of(p))), dim3(512),
+                     kLds, stream, p);
   return hipGetLastError();
 }
 
 template <int KD>
-hipError_t go_k(const LinParams& p, bool bf16, int rows, hipStream_t stream) {
-  if (!bf16) return go<false, KD, 1, false>(p, stream);
-  if (rows == 128) {
-    if (p.hi_lo) return go<true, KD, 2, true>(p, stream);
-    return go<true, KD, 2, false>(p, stream);
-  }
-  if (p.hi_lo) return go<true, KD, 1, true>(p, stream);
-  return go<true, KD, 1, false>(p, stream);
+hipError_t go_k(const LinParams& p, bool bf16, hipStream_t stream) {
+  if (bf16) return p.hi_lo ? go<KD, true>(p, stream) : go<KD, false>(p, stream);
+  hipLaunchKernelGGL((linear_states_f32_kernel<KD>), dim3(static_cast<unsigned>(grid_of(p))), dim3(256), 0,
+                     stream, p);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_linear_states(const LinParams& p, int k_dim, bool io_bf16, int value_block,
-                                hipStream_t stream) {
-  return k_dim == 128 ? go_k<128>(p, io_bf16, value_block, stream)
-                      : go_k<64>(p, io_bf16, value_block, stream);
+hipError_t launch_linear_states(const LinParams& p, int k_dim, bool io_bf16, hipStream_t stream) {
+  return k_dim == 128 ? go_k<128>(p, io_bf16, stream) : go_k<64>(p, io_bf16, stream);
 }
 
 hipError_t launch_linear_scan(const LinParams& p, int k_dim, hipStream_t stream) {

@@ -61,11 +61,12 @@ kda_status linear_shape(const kda_linear_args* a) {
     return fail(KDA_ERR_SHAPE, "K=%lld, only 64 and 128 are supported", (long long)a->K);
   if (a->V < 64 || a->V > 512 || a->V % 64)
     return fail(KDA_ERR_SHAPE, "V=%lld is not a multiple of 64 up to 512", (long long)a->V);
-  if (a->B < 1 || a->B > (int64_t(1) << 31) || a->T < 0 || a->T > kBig || a->N < 0 ||
+  if (a->B < 1 || a->B > (int64_t(1) << 31) || a->T < 0 || a->T > (int64_t(1) << 36) || a->N < 0 ||
       a->N > (int64_t(1) << 31))
     return fail(KDA_ERR_SHAPE, "bad B=%lld T=%lld N=%lld", (long long)a->B, (long long)a->T,
                 (long long)a->N);
-  if (a->H < 1 || a->H > 65535) return fail(KDA_ERR_SHAPE, "H=%lld", (long long)a->H);
+  if (a->H < 1 || a->H * a->V > (1 << 22))  // a chunk's rows of o stay within 2^31 bytes
+    return fail(KDA_ERR_SHAPE, "H=%lld is not positive, or H*V exceeds 2^22", (long long)a->H);
   if (a->Hk < 1 || a->Hk > a->H || a->H % a->Hk)
     return fail(KDA_ERR_SHAPE, "Hk=%lld does not divide H=%lld", (long long)a->Hk, (long long)a->H);
   if (a->cu_seqlens) {
@@ -118,7 +119,6 @@ struct LinPlan {
 
 LinPlan linear_plan(const kda_linear_args* a) {
   LinPlan pl{};
-  const bool bf16 = a->io_dtype == KDA_BF16;
   if (linear_token_form(a)) {
     pl.tokens = true;
     const int least = a->K == 128 ? 16 : 32;
@@ -129,16 +129,46 @@ LinPlan linear_plan(const kda_linear_args* a) {
     pl.segs = 1;
     return pl;
   }
-  pl.rows = bf16 && a->V % 128 == 0 ? 128 : 64;
-  const int64_t blocks = a->H * (a->V / pl.rows);
+  // The chunked form's geometry: the cheapest by a model of the time, in microseconds, with
+  // the costs of a 64-token step as measured on one MI355X (BF16 I/O, K = V = 128; FP32 I/O
+  // about five times that). A compute unit takes one workgroup at a time.
+  //   serial    6 + steps x 1.33 (64 value rows) or 1.85 (128) x rounds of 256 workgroups
+  //   segments 16 + steps of a segment x 2.7 (64) or 5 (128), both passes and the scan, at
+  //            as many segments as one round holds
+  // E.g. T = 8192: H = 6 37 us by 64-row segments, 170 serial; H = 48 148 us by 128-row
+  // segments, 187 by 64-row ones, 228 serial; H = 96 248 us serial by 64 rows, 283 by 128,
+  // 243 (two 128-row segments and a workspace). T = 1024: H = 6 22 us by segments, 25
+  // serial; H = 48 27 us serial, 35 by segments.
+  constexpr int64_t kUnits = 256;  // compute units
+  const bool bf16 = a->io_dtype == KDA_BF16;
+  const double slow = bf16 ? 1.0 : 5.0;
+  // 128 rows of an FP32 state (its updates in two parts) do not fit the registers
+  const int most = bf16 && a->state_dtype == KDA_BF16 && a->V % 128 == 0 ? 128 : 64;
+  // a packed batch's longest sequence is taken for 1.75 times the mean
+  const double steps = a->cu_seqlens && a->N > 1
+                           ? std::fmin(1.0, 1.75 / static_cast<double>(a->N)) * static_cast<double>(a->T) / 64
+                           : static_cast<double>(a->T) / 64;
+  double best = 1e300;
   int64_t seg = 0;
-  if (a->segment_tokens > 0) {
-    seg = a->segment_tokens;
-  } else if (a->segment_tokens == 0 && a->N * blocks < 256) {
-    const int64_t tokens = a->cu_seqlens ? a->T : a->N * a->T;
-    seg = ceil_div(ceil_div(tokens * blocks, 512), kda::kLinChunk) * kda::kLinChunk;
-    if (seg < 128) seg = 128;
+  for (int rows = 64; rows <= most; rows *= 2) {
+    const int64_t blocks = a->H * (a->V / rows), wgs = a->N * blocks;
+    const double serial = 6 + steps * (rows == 64 ? 1.33 : 1.85) * slow * static_cast<double>(ceil_div(wgs, kUnits));
+    if (serial < best) {
+      best = serial;
+      pl.rows = rows;
+      seg = 0;
+    }
+    if (a->segment_tokens != 0 || wgs > kUnits / 2) continue;
+    int64_t len = a->cu_seqlens ? ceil_div(a->T * blocks, kUnits - wgs) : ceil_div(a->T, kUnits / wgs);
+    len = ceil_div(len < 128 ? 128 : len, kda::kLinChunk) * kda::kLinChunk;
+    const double cut = 16 + static_cast<double>(len / 64) * (rows == 64 ? 2.7 : 5.0) * slow;
+    if (len < a->T && cut < best) {
+      best = cut;
+      pl.rows = rows;
+      seg = len;
+    }
   }
+  if (a->segment_tokens > 0) seg = a->segment_tokens;
   if (seg >= a->T) seg = 0;
   pl.seg = seg;
   if (seg == 0) {
@@ -456,6 +486,7 @@ kda_status kda_linear(const kda_linear_args* a, void* stream_) {
     p.vs[d] = a->v_stride[d];
   }
   p.scale = a->scale > 0.0f ? a->scale : 1.0f / std::sqrt(static_cast<float>(a->K));
+  p.log2_scale = std::log2(static_cast<double>(p.scale));
   p.g_bf16 = a->g_dtype == KDA_BF16;
   p.st_bf16 = a->state_dtype == KDA_BF16;
   p.hi_lo = bf16 && !p.st_bf16;
@@ -474,6 +505,7 @@ kda_status kda_linear(const kda_linear_args* a, void* stream_) {
   p.segs_per_seq = pl.segs;
   p.slots = pl.slots;
   p.segmented = pl.seg ? 1 : 0;
+  p.longest_first = a->cu_seqlens && !pl.seg && a->N > 1 && a->N <= 64;
   p.scan_s = static_cast<float*>(a->workspace);
   p.scan_d = reinterpret_cast<float*>(static_cast<unsigned char*>(a->workspace) + pl.scan_d);
   p.vblocks = static_cast<int32_t>(a->V / pl.rows);
@@ -481,7 +513,9 @@ kda_status kda_linear(const kda_linear_args* a, void* stream_) {
   p.tasks = pl.slots * a->H;
   hipError_t e = hipSuccess;
   if (pl.seg) {
-    e = kda::launch_linear_states(p, k_dim, bf16, pl.rows, stream);
+    kda::LinParams ps = p;
+    ps.vblocks = static_cast<int32_t>(a->V / kda::kLinRows);
+    e = kda::launch_linear_states(ps, k_dim, bf16, stream);
     if (e == hipSuccess) e = kda::launch_linear_scan(p, k_dim, stream);
   }
   if (e == hipSuccess) e = kda::launch_linear_chunks(p, k_dim, bf16, pl.rows, stream);

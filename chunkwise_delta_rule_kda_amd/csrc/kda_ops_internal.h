@@ -13,6 +13,7 @@ namespace kda {
 kda_status set_error(kda_status s, const char* text) noexcept;
 
 constexpr int kLinChunk = 64;       // tokens per chunk
+constexpr int kLinRows = 64;        // state rows (values) per workgroup of the chunked form
 constexpr int kLinDecodeMaxT = 8;   // longest fixed-layout call of the token loop
 
 struct LinParams {
@@ -29,6 +30,7 @@ struct LinParams {
   int32_t H, Hk, V;
   int64_t qs[3], ks[3], vs[3];  // strides in elements: batch, token, head
   float scale;
+  double log2_scale;
   int32_t g_bf16, st_bf16;
   int32_t hi_lo;             // FP32 states of BF16 inputs: the decayed values in two parts
   const int32_t* in_idx;     // pool slots read and written (null: sequence n at n)
@@ -41,6 +43,7 @@ struct LinParams {
   int64_t segs_per_seq;      // fixed layout
   int64_t slots;             // bound on w; the serial form has one per sequence
   int32_t segmented;
+  int32_t longest_first;     // serial varlen form: workgroups by decreasing sequence length
   float* scan_s;             // FP32 [H][slots][V][K]
   float* scan_d;             // FP32 [H][slots]: the segment's total decay
   // Grid: tasks of `sub` workgroups each (sub = heads per task * value blocks), a task's
@@ -49,10 +52,9 @@ struct LinParams {
   int64_t tasks;
 };
 
-hipError_t launch_linear_chunks(const LinParams& p, int k_dim, bool io_bf16, int value_block,
+hipError_t launch_linear_chunks(const LinParams& p, int k_dim, bool io_bf16, int rows,
                                 hipStream_t stream);
-hipError_t launch_linear_states(const LinParams& p, int k_dim, bool io_bf16, int value_block,
-                                hipStream_t stream);
+hipError_t launch_linear_states(const LinParams& p, int k_dim, bool io_bf16, hipStream_t stream);
 hipError_t launch_linear_scan(const LinParams& p, int k_dim, hipStream_t stream);
 // rows: state rows per workgroup (16 to 128)
 hipError_t launch_linear_tokens(const LinParams& p, int k_dim, bool io_bf16, int rows,

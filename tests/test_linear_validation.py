@@ -69,8 +69,8 @@ def test_valid_calls_pass():
     (dict(q=None), 1), (dict(k=None), 1), (dict(v=None), 1), (dict(o=None), 1),
     (dict(K=96), 2), (dict(K=256), 2), (dict(V=32), 2), (dict(V=100), 2), (dict(V=576), 2),
     (dict(H=0, Hk=1), 2), (dict(Hk=3), 2), (dict(Hk=8), 2), (dict(Hk=-1), 2), (dict(T=-1), 2),
-    (dict(B=0), 2), (dict(N=2), 2), (dict(T=(1 << 40) + 1), 2), (dict(H=70000), 2),
-    (dict(T=1 << 40, H=60000), 2), (dict(B=1 << 31, N=1 << 31), 2),
+    (dict(B=0), 2), (dict(N=2), 2), (dict(T=(1 << 36) + 1), 2), (dict(H=70000), 2),
+    (dict(T=1 << 36, H=30000), 2), (dict(H=1 << 33), 2), (dict(B=1 << 31, N=1 << 31), 2),
     (dict(io_dtype=2), 3), (dict(state_dtype=-1), 3), (dict(g_dtype=5), 3),
     (dict(scale=float("nan")), 5), (dict(scale=-1.0), 5),
     (dict(segment_tokens=63), 10), (dict(segment_tokens=1 << 41), 10),
