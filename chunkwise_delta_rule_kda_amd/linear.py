@@ -3,7 +3,7 @@
 import ctypes
 
 from . import KdaError, _raise_if, kda_last_error, load_library
-from ._tensors import dtype_code, is_tensor, need, on_device, run_on, steps
+from ._tensors import dtype_code, get_torch, is_tensor, need, on_device, run_on
 
 __all__ = ["kda_linear", "kda_linear_args", "kda_linear_check", "kda_linear_plan",
            "kda_linear_workspace_bytes", "make_linear_args"]
@@ -71,9 +71,11 @@ def kda_linear_plan(args):
     return {f: getattr(info, f) for f, _ in kda_linear_plan_info._fields_}
 
 
-def _state_shape(t, name, shape, dtype):
-    need(tuple(t.shape) == shape, 2, f"{name} has shape {tuple(t.shape)}, expected {shape}")
-    need(t.dtype == dtype, 3, f"{name} is {t.dtype}, the state dtype is {dtype}")
+def _state_check(t, name, shape, dtype):
+    if t.shape != shape:
+        raise KdaError(2, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise KdaError(3, f"{name} is {t.dtype}, the state dtype is {dtype}")
 
 
 def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=None, scale=None,
@@ -101,106 +103,123 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
     Ids outside the pool start from zero and write nothing.
     Returns (o, state_out or None).
     """
-    import torch
-
+    torch = get_torch()
     is_tensor(q, "q")
     is_tensor(k, "k")
     is_tensor(v, "v")
-    need(q.dim() == 4 and v.dim() == 4, 2, "q and v must have four axes, [B, T, heads, dim]")
-    B, T, Hk, K = q.shape
-    H, V = v.shape[2:]
+    if q.dim() != 4 or v.dim() != 4:
+        raise KdaError(2, "q and v must have four axes, [B, T, heads, dim]")
+    shape = q.shape
+    B, T, Hk, K = shape
+    vB, vT, H, V = v.shape
     io = dtype_code(q, "q")
     dt = q.dtype
-    need(k.shape == q.shape, 2, f"k has shape {tuple(k.shape)}, expected {tuple(q.shape)}")
-    need(v.shape[:2] == q.shape[:2], 2, f"v has shape {tuple(v.shape)}, expected "
-         f"({B}, {T}, heads, dim)")
-    need(k.dtype == dt and v.dtype == dt, 3, f"q, k, v are {dt}, {k.dtype}, {v.dtype}")
-    need(Hk >= 1 and H >= 1 and H % Hk == 0, 2, f"{Hk} q/k heads do not divide {H} heads")
-    sq, sk, sv = steps(q), steps(k), steps(v)
-    need(T == 0 or B == 0 or (sq[3] == 1 and sk[3] == 1 and sv[3] == 1), 2,
-         "the last axis of q, k and v must be contiguous")
+    if k.shape != shape:
+        raise KdaError(2, f"k has shape {tuple(k.shape)}, expected {tuple(shape)}")
+    if vB != B or vT != T:
+        raise KdaError(2, f"v has shape {tuple(v.shape)}, expected ({B}, {T}, heads, dim)")
+    if k.dtype != dt or v.dtype != dt:
+        raise KdaError(3, f"q, k, v are {dt}, {k.dtype}, {v.dtype}")
+    if Hk < 1 or H < 1 or H % Hk:
+        raise KdaError(2, f"{Hk} q/k heads do not divide {H} heads")
+    sq, sk, sv = q.stride(), k.stride(), v.stride()
+    if (sq[3] != 1 or sk[3] != 1 or sv[3] != 1) and B and T:
+        raise KdaError(2, "the last axis of q, k and v must be contiguous")
+    if B == 1 or T == 1 or Hk == 1 or H == 1:  # the stride of an axis of one entry says nothing
+        one = [n == 1 for n in (B, T, Hk, H)]
+        sq, sk = ([0 if o else x for o, x in zip(one[:3], st)] for st in (sq, sk))
+        sv = [0 if o else x for o, x in zip((one[0], one[1], one[3]), sv)]
     N = B
     if cu_seqlens is not None:
         is_tensor(cu_seqlens, "cu_seqlens", torch.int64)
         need(cu_seqlens.dim() == 1 and cu_seqlens.numel() >= 2, 2,
              "cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
         need(cu_seqlens.is_contiguous(), 2, "cu_seqlens must be contiguous")
-        need(B == 1, 2, f"packed varlen needs B = 1 (got {B})")
+        if not (B == 1):
+            raise KdaError(2, f"packed varlen needs B = 1 (got {B})")
         N = cu_seqlens.numel() - 1
     gt = 1
     if g is not None:
         is_tensor(g, "g")
         gt = dtype_code(g, "g")
-        need(gt == 1 or gt == io, 3, f"g is {g.dtype}, expected {dt} or float32")
-        need(tuple(g.shape) == (B, T, H), 2, f"g has shape {tuple(g.shape)}, expected "
-             f"{(B, T, H)}")
-        need(g.is_contiguous(), 2, "g must be contiguous")
+        if gt != 1 and gt != io:
+            raise KdaError(3, f"g is {g.dtype}, expected {dt} or float32")
+        if g.shape != (B, T, H):
+            raise KdaError(2, f"g has shape {tuple(g.shape)}, expected {(B, T, H)}")
+        if not g.is_contiguous():
+            raise KdaError(2, "g must be contiguous")
     if log_decay is not None:
         is_tensor(log_decay, "log_decay", torch.float32)
-        need(tuple(log_decay.shape) == (H,) and log_decay.is_contiguous(), 2,
-             f"log_decay must be a contiguous [{H}]")
+        if not (log_decay.shape == (H,) and log_decay.is_contiguous()):
+            raise KdaError(2, f"log_decay must be a contiguous [{H}]")
     if state_dtype is None:
         state_dtype = state_in.dtype if state_in is not None else dt
-    need(state_dtype in (torch.bfloat16, torch.float32), 3, f"state dtype {state_dtype}")
+    st_code = 0 if state_dtype == torch.bfloat16 else 1
+    if st_code and state_dtype != torch.float32:
+        raise KdaError(3, f"state dtype {state_dtype}")
     slots = pitch = 0
     if ssm_state_indices is not None:
         need(state_in is not None, 10, "a state pool needs state_in")
+        is_tensor(state_in, "state_in")
         need(state_in.dim() == 4 and state_in.shape[0] >= 1, 2,
              "a state pool needs state_in [slots, H, V, K]")
         slots = state_in.shape[0]
-        _state_shape(state_in, "the state pool", (slots, H, V, K), state_dtype)
+        _state_check(state_in, "the state pool", (slots, H, V, K), state_dtype)
         st = state_in.stride()
-        need(st[3] == 1 and st[2] == K and (H == 1 or st[1] == V * K), 2,
-             "each state pool slot must be contiguous")
+        if st[3] != 1 or st[2] != K or (H > 1 and st[1] != V * K):
+            raise KdaError(2, "each state pool slot must be contiguous")
         pitch = st[0] if slots > 1 else H * V * K
-        need(pitch % 8 == 0, 2, "the state pool's slot pitch must be a multiple of 8 elements")
-        need(state_out is None or state_out is state_in
-             or state_out.data_ptr() == state_in.data_ptr(), 6,
-             "with a state pool, state_out must be None or state_in")
+        if pitch % 8:
+            raise KdaError(2, "the state pool's slot pitch must be a multiple of 8 elements")
+        if (state_out is not None and state_out is not state_in
+                and state_out.data_ptr() != state_in.data_ptr()):
+            raise KdaError(6, "with a state pool, state_out must be None or state_in")
         state_out = state_in
         for name, ids in (("ssm_state_indices", ssm_state_indices),
                           ("state_out_indices", state_out_indices)):
             if ids is not None:
                 is_tensor(ids, name, torch.int32)
-                need(tuple(ids.shape) == (N,) and ids.is_contiguous(), 2,
-                     f"{name} must be a contiguous [{N}]")
+                if ids.shape != (N,) or not ids.is_contiguous():
+                    raise KdaError(2, f"{name} must be a contiguous [{N}]")
     else:
         need(state_out_indices is None, 10, "state_out_indices needs ssm_state_indices")
-        if state_in is not None:
-            _state_shape(state_in, "state_in", (N, H, V, K), state_dtype)
-            need(state_in.is_contiguous(), 2, "state_in must be contiguous")
-        if state_out is not None:
-            _state_shape(state_out, "state_out", (N, H, V, K), state_dtype)
-            need(state_out.is_contiguous(), 2, "state_out must be contiguous")
+        for name, t in (("state_in", state_in), ("state_out", state_out)):
+            if t is not None:
+                is_tensor(t, name)
+                _state_check(t, name, (N, H, V, K), state_dtype)
+                if not t.is_contiguous():
+                    raise KdaError(2, f"{name} must be contiguous")
     if o is not None:
-        need(o.shape == v.shape and o.dtype == dt and o.is_contiguous(), 2,
-             f"o must be a contiguous {tuple(v.shape)} of {dt}")
+        is_tensor(o, "o")
+        if not (o.shape == v.shape and o.dtype == dt and o.is_contiguous()):
+            raise KdaError(2, f"o must be a contiguous {tuple(v.shape)} of {dt}")
     if workspace is not None:
         need(workspace.is_contiguous(), 2, "workspace must be contiguous")
-    dev = q.device
-    on_device(dev, q=q, k=k, v=v, g=g, log_decay=log_decay, state_in=state_in,
-              cu_seqlens=cu_seqlens, o=o, state_out=state_out, workspace=workspace,
-              ssm_state_indices=ssm_state_indices, state_out_indices=state_out_indices)
+    dev = on_device(q, "q k v g log_decay state_in cu_seqlens o state_out workspace "
+                    "ssm_state_indices state_out_indices", k, v, g, log_decay, state_in, cu_seqlens,
+                    o, state_out, workspace, ssm_state_indices, state_out_indices)
     lib = load_library()
     with run_on(dev, stream) as handle:
         if o is None:
-            o = torch.empty((B, T, H, V), dtype=dt, device=dev)
+            o = v.new_empty(v.shape)
         if state_out is None and output_final_state:
-            state_out = torch.empty((N, H, V, K), dtype=state_dtype, device=dev)
+            state_out = v.new_empty((N, H, V, K), dtype=state_dtype)
         a = kda_linear_args(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(log_decay), _ptr(state_in),
             _ptr(cu_seqlens), o.data_ptr(), _ptr(state_out), None, 0, B, T, H, Hk, K, V, N,
-            sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], io,
-            0 if state_dtype == torch.bfloat16 else 1, gt, 0.0 if scale is None else scale,
-            segment_tokens, _ptr(ssm_state_indices), _ptr(state_out_indices), slots, pitch)
-        if workspace is None:
-            size = kda_linear_workspace_bytes(a)
-            if size:
-                workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+            sq[0], sq[1], sq[2], sk[0], sk[1], sk[2], sv[0], sv[1], sv[2], io, st_code, gt,
+            0.0 if scale is None else scale, segment_tokens, _ptr(ssm_state_indices),
+            _ptr(state_out_indices), slots, pitch)
+        ref = ctypes.byref(a)
         if workspace is not None:
             a.workspace = workspace.data_ptr()
             a.workspace_bytes = workspace.numel() * workspace.element_size()
-        status = lib.kda_linear(ctypes.byref(a), handle)
+        status = lib.kda_linear(ref, handle)
+        if status == 7 and workspace is None:  # the call needs one: refused before any launch
+            workspace = torch.empty(kda_linear_workspace_bytes(a), dtype=torch.uint8, device=dev)
+            a.workspace = workspace.data_ptr()
+            a.workspace_bytes = workspace.numel()
+            status = lib.kda_linear(ref, handle)
     if status:
         raise KdaError(status, kda_last_error())
     return o, state_out

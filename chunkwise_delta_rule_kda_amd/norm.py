@@ -4,7 +4,7 @@ kda_gated_norm (include/kda.h)."""
 import ctypes
 
 from . import KdaError, kda_last_error, load_library
-from ._tensors import dtype_code, is_tensor, need, on_device, run_on
+from ._tensors import dtype_code, get_torch, is_tensor, need, on_device, run_on
 
 __all__ = ["kda_gated_norm", "kda_gated_norm_args"]
 
@@ -26,7 +26,10 @@ _ACT = {"sigmoid": 0, "silu": 1}
 def _rows(t, name):
     """Strides of the rows of t seen as [M, G, D] with G its last axis but one."""
     shape, stride = t.shape, t.stride()
-    need(shape[-1] == 1 or stride[-1] == 1, 2, f"the last axis of {name} must be contiguous")
+    if t.is_contiguous():
+        return (stride[-3], stride[-2]) if len(shape) > 2 else (shape[-1], 0)
+    if not (shape[-1] == 1 or stride[-1] == 1):
+        raise KdaError(2, f"the last axis of {name} must be contiguous")
     g = stride[-2] if len(shape) > 2 and shape[-2] > 1 else 0
     m, span = 0, 1  # stride of the collapsed leading axes, rows they span so far
     for n, s in zip(reversed(shape[:-2] if len(shape) > 2 else shape[:-1]),
@@ -35,7 +38,8 @@ def _rows(t, name):
             continue
         if span == 1:
             m = s
-        need(s == m * span, 2, f"the leading axes of {name} cannot be seen as one")
+        if not (s == m * span):
+            raise KdaError(2, f"the leading axes of {name} cannot be seen as one")
         span *= n
     return m, g
 
@@ -54,44 +58,45 @@ def kda_gated_norm(x, gate=None, weight=None, residual=None, *, next_weight=None
     gate_act: "sigmoid" or "silu". out may be x, gate or residual itself where that is
     contiguous. Returns y, or (y, z).
     """
-    import torch
-
+    torch = get_torch()
     is_tensor(x, "x")
     need(x.dim() >= 1, 2, "x must have at least one axis")
     code = dtype_code(x, "x")
     shape, dt = x.shape, x.dtype
     D = shape[-1]
-    need(gate_act in _ACT, 4, f"gate_act {gate_act!r} is neither 'sigmoid' nor 'silu'")
+    if not (gate_act in _ACT):
+        raise KdaError(4, f"gate_act {gate_act!r} is neither 'sigmoid' nor 'silu'")
     G = shape[-2] if len(shape) > 2 else 1
-    need(D >= 1 and G >= 1, 2, f"x has shape {tuple(shape)}")
+    if not (D >= 1 and G >= 1):
+        raise KdaError(2, f"x has shape {tuple(shape)}")
     M = x.numel() // (D * G)
     st = [0] * 6
     for i, (name, t) in enumerate((("x", x), ("gate", gate), ("residual", residual))):
         if t is None:
             continue
         is_tensor(t, name, dt)
-        need(t.shape == shape, 2, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if not (t.shape == shape):
+            raise KdaError(2, f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         st[2 * i:2 * i + 2] = _rows(t, name)
     for name, t in (("weight", weight), ("next_weight", next_weight)):
         if t is not None:
             is_tensor(t, name, torch.float32)
-            need(tuple(t.shape) == (D,) and t.is_contiguous(), 2,
-                 f"{name} must be a contiguous [{D}]")
+            if not (tuple(t.shape) == (D,) and t.is_contiguous()):
+                raise KdaError(2, f"{name} must be a contiguous [{D}]")
     for name, t in (("out", out), ("next_out", next_out)):
         if t is not None:
             is_tensor(t, name, dt)
-            need(t.shape == shape and t.is_contiguous(), 2,
-                 f"{name} must be a contiguous {tuple(shape)}")
-    dev = x.device
-    on_device(dev, x=x, gate=gate, weight=weight, residual=residual, next_weight=next_weight,
-              out=out, next_out=next_out)
+            if not (t.shape == shape and t.is_contiguous()):
+                raise KdaError(2, f"{name} must be a contiguous {tuple(shape)}")
+    dev = on_device(x, "x gate weight residual next_weight out next_out", gate, weight, residual,
+                    next_weight, out, next_out)
     both = next_weight is not None or next_out is not None
     ptr = lambda t: None if t is None else t.data_ptr()
     with run_on(dev, stream) as handle:
         if out is None:
-            out = torch.empty(shape, dtype=dt, device=dev)
+            out = x.new_empty(shape)
         if both and next_out is None:
-            next_out = torch.empty(shape, dtype=dt, device=dev)
+            next_out = x.new_empty(shape)
         a = kda_gated_norm_args(ptr(x), ptr(gate), ptr(residual), ptr(weight), ptr(next_weight),
                                 ptr(out), ptr(next_out), M, G, D, *st, code, _ACT[gate_act], eps,
                                 scale)

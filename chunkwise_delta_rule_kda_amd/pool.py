@@ -3,7 +3,7 @@
 import ctypes
 
 from . import KdaError, kda_last_error, load_library
-from ._tensors import dtype_code, is_tensor, need, on_device, run_on
+from ._tensors import dtype_code, get_torch, is_tensor, need, on_device, run_on
 
 __all__ = ["kda_pool", "kda_pool_copy", "kda_pool_copy_args", "kda_pool_compact",
            "kda_pool_compact_args", "KDA_POOL_COMPACT_SLOTS"]
@@ -30,17 +30,20 @@ class kda_pool_compact_args(ctypes.Structure):
 
 def _pool_of(t, name, layered):
     """[slots, ...] (or [layers, slots, ...]) with contiguous slots, as a kda_pool."""
+    get_torch()
     is_tensor(t, name)
     code = dtype_code(t, name)
     axis = 1 if layered else 0
-    need(t.dim() >= axis + 2, 2, f"{name} must be [{'layers, ' if layered else ''}slots, ...]")
+    if not (t.dim() >= axis + 2):
+        raise KdaError(2, f"{name} must be [{'layers, ' if layered else ''}slots, ...]")
     shape, stride = t.shape, t.stride()
     elems = 1
     for n, s in zip(reversed(shape[axis + 1:]), reversed(stride[axis + 1:])):
-        need(n == 1 or s == elems, 2, f"each slot of {name} must be contiguous")
+        if not (n == 1 or s == elems):
+            raise KdaError(2, f"each slot of {name} must be contiguous")
         elems *= n
-    need(elems >= 1 and shape[axis] >= 1 and (not layered or shape[0] >= 1), 2,
-         f"{name} is empty")
+    if not (elems >= 1 and shape[axis] >= 1 and (not layered or shape[0] >= 1)):
+        raise KdaError(2, f"{name} is empty")
     pitch = stride[axis] if shape[axis] > 1 else elems
     layers = shape[0] if layered else 1
     return kda_pool(t.data_ptr(), shape[axis], layers, elems, pitch,
@@ -48,10 +51,9 @@ def _pool_of(t, name, layered):
 
 
 def _index(t, name):
-    import torch
-
-    is_tensor(t, name, torch.int32)
-    need(t.dim() == 1 and t.is_contiguous(), 2, f"{name} must be a contiguous 1-D tensor")
+    is_tensor(t, name, get_torch().int32)
+    if not (t.dim() == 1 and t.is_contiguous()):
+        raise KdaError(2, f"{name} must be a contiguous 1-D tensor")
 
 
 def kda_pool_copy(pool, src, dst, *, source=None, layered=False, stream=None):
@@ -72,9 +74,9 @@ def kda_pool_copy(pool, src, dst, *, source=None, layered=False, stream=None):
          "pool and source differ in their layers or slots")
     _index(src, "src")
     _index(dst, "dst")
-    need(src.numel() == dst.numel(), 2, f"src has {src.numel()} ids, dst {dst.numel()}")
-    dev = pool.device
-    on_device(dev, pool=pool, source=source, src=src, dst=dst)
+    if not (src.numel() == dst.numel()):
+        raise KdaError(2, f"src has {src.numel()} ids, dst {dst.numel()}")
+    dev = on_device(pool, "pool source src dst", source, src, dst)
     a = kda_pool_copy_args(s, d, src.data_ptr(), dst.data_ptr(), src.numel())
     with run_on(dev, stream) as handle:
         status = load_library().kda_pool_copy(ctypes.byref(a), handle)
@@ -94,22 +96,21 @@ def kda_pool_compact(pool, slots, *, new_slots=None, count=None, workspace=None,
     new_slots may be `slots` itself. Everything happens on the device: nothing is read
     back to the host. A pool has at most KDA_POOL_COMPACT_SLOTS slots here.
     """
-    import torch
-
+    torch = get_torch()
     p = _pool_of(pool, "pool", layered)
     _index(slots, "slots")
     n = slots.numel()
     if new_slots is not None:
         _index(new_slots, "new_slots")
-        need(new_slots.numel() == n, 2, f"new_slots must have {n} entries")
+        if not (new_slots.numel() == n):
+            raise KdaError(2, f"new_slots must have {n} entries")
     if count is not None:
         _index(count, "count")
         need(count.numel() == 1, 2, "count must have one entry")
     if workspace is not None:
         need(workspace.is_contiguous(), 2, "workspace must be contiguous")
-    dev = pool.device
-    on_device(dev, pool=pool, slots=slots, new_slots=new_slots, count=count,
-              workspace=workspace)
+    dev = on_device(pool, "pool slots new_slots count workspace", slots, new_slots, count,
+                    workspace)
     lib = load_library()
     with run_on(dev, stream) as handle:
         if new_slots is None:
