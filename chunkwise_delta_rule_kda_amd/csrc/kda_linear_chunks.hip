@@ -113,154 +113,131 @@ __device__ __forceinline__ void by_wave(int wave, F f) {
   }
 }
 
-// FP32 I/O.
+// FP32 I/O, FP32 MFMA (an eighth of the BF16 rate), which bounds it: 12288 clocks of products
+// per SIMD and chunk. Four waves hold the next chunk's tiles in registers, write them to LDS,
+// and form the scores beside the other four's products with the state; those add P V while
+// the next tiles are written.
 template <int KD>
-__global__ __launch_bounds__(256) void linear_f32_kernel(LinParams p) {
-  typedef F32x8 Frag;
-  constexpr bool BF16 = false, LOW = false;
-  constexpr int NC = 1, kEs = 4;
-  constexpr int R = 64 * NC;
-  constexpr int KB = KD / 32;
-  constexpr int kPprK = KD * kEs / 16, kPprV = R * kEs / 16;
-  __shared__ __align__(16) unsigned char q_tile[64 * KD * kEs];
-  __shared__ __align__(16) unsigned char k_tile[64 * KD * kEs];
-  __shared__ __align__(16) unsigned char v_tile[64 * R * kEs];
-  __shared__ __align__(16) unsigned char p_tile[kScoreBytes<BF16>];
-  __shared__ Gates gates;
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_f32_kernel(LinParams p) {
+  constexpr int R = kLinRows;
+  constexpr int kPprK = KD / 4, kPprV = R / 4;
+  extern __shared__ __align__(1024) unsigned char lds[];
+  unsigned char* const q_tile = lds;
+  unsigned char* const k_tile = q_tile + 64 * KD * 4;
+  unsigned char* const v_tile = k_tile + 64 * KD * 4;
+  unsigned char* const p_tile = v_tile + 64 * R * 4;
+  Gates& gates = *reinterpret_cast<Gates*>(p_tile + kScoreBytes<false>);
 
   LinTask task;
   if (!find_task(p, task)) return;  // uniform
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6) & 3;
   const int grp = lane >> 4, m = lane & 15;
-  const int hk = task.h / (p.H / p.Hk);
-  const int row0 = task.vblk * R + wave * 16 * NC;  // the wave's first value row
-  const unsigned char* qp = static_cast<const unsigned char*>(p.q) +
-                            (row_offset(p, p.qs, task.n, task.tok0) + hk * p.qs[2]) * kEs;
-  const unsigned char* kp = static_cast<const unsigned char*>(p.k) +
-                            (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * kEs;
-  const unsigned char* vp = static_cast<const unsigned char*>(p.v) +
-                            (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * kEs;
-  const uint32_t qpitch = static_cast<uint32_t>(p.qs[1] * kEs);
-  const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * kEs);
-  const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * kEs);
-
-  Tile<kPprK> qt, kt;
-  Tile<kPprV> vt;
-  const float fixed = p.log_decay ? p.log_decay[task.h] : 0.f;
-  float x = 0.f;
-  auto fetch = [&](int64_t at) {
-    const int left = static_cast<int>(task.len - at < 64 ? task.len - at : 64);
-    qt.load(qp + at * qpitch, qpitch, left, tid);
-    kt.load(kp + at * kpitch, kpitch, left, tid);
-    vt.load(vp + at * vpitch, vpitch, left, tid);
-    const int i = 16 * wave + m;
-    x = load_log_decay(p, task.tok0 + at + (i < left ? i : left - 1), task.h);
-  };
-  if (task.len > 0) fetch(0);
-
-  // Start state: the scan's, or the sequence's own.
-  f32x4 S[KD / 16][NC];
-  const int64_t head_state = static_cast<int64_t>(task.h) * p.V * KD;
-  if (p.segmented && !(task.first && task.last)) {
-    load_state(S, p.scan_s, (static_cast<int64_t>(task.h) * p.slots + task.slot) * p.V * KD, false, KD,
-               row0, grp, m);
-  } else {
-    const int64_t slot = p.in_idx ? p.in_idx[task.n] : task.n;
-    if (p.state_in && slot >= 0 && slot < p.pool_slots) {
-      load_state(S, p.state_in, slot * p.slot_pitch + head_state, p.st_bf16, KD, row0, grp, m);
-    } else {
-#pragma unroll
-      for (int t = 0; t < KD / 16; ++t)
-#pragma unroll
-        for (int c = 0; c < NC; ++c) S[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-  }
+  const int chunks = static_cast<int>((task.len + 63) >> 6);
+  const int tail = static_cast<int>(task.len - 64 * static_cast<int64_t>(chunks - 1));
   // The tiles of P above the diagonal that an operand read covers are zero throughout.
-  for (int i = tid; i < kScoreBytes<BF16> / 16; i += 256) {
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    *reinterpret_cast<u32x4*>(p_tile + 16 * i) = zero;
+  for (int i = tid; i < kScoreBytes<false> / 16; i += 512)
+    *reinterpret_cast<u32x4*>(p_tile + 16 * i) = u32x4{0u, 0u, 0u, 0u};
+
+  if (__builtin_amdgcn_readfirstlane(tid >> 8) != 0) {
+    __builtin_amdgcn_s_setprio(2);
+    const int hk = task.h / (p.H / p.Hk), t = tid & 255;
+    const unsigned char* qp = static_cast<const unsigned char*>(p.q) +
+                              (row_offset(p, p.qs, task.n, task.tok0) + hk * p.qs[2]) * 4;
+    const unsigned char* kp = static_cast<const unsigned char*>(p.k) +
+                              (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * 4;
+    const unsigned char* vp = static_cast<const unsigned char*>(p.v) +
+                              (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * 4;
+    const uint32_t qpitch = static_cast<uint32_t>(p.qs[1] * 4);
+    const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * 4);
+    const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * 4);
+    Tile<kPprK> qt, kt;
+    Tile<kPprV> vt;
+    const float fixed = p.log_decay ? p.log_decay[task.h] : 0.f;
+    float x = 0.f;
+    auto fetch = [&](int chunk) {
+      const int rows = chunk + 1 < chunks ? 64 : tail, i = 16 * wave + m;
+      const int64_t at = 64 * static_cast<int64_t>(chunk);
+      qt.load(qp + at * qpitch, qpitch, rows, t);
+      kt.load(kp + at * kpitch, kpitch, rows, t);
+      vt.load(vp + at * vpitch, vpitch, rows, t);
+      x = load_log_decay(p, task.tok0 + at + (i < rows ? i : rows - 1), task.h);
+    };
+    if (chunks > 0) fetch(0);
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      qt.store(q_tile, t);
+      kt.store(k_tile, t);
+      vt.store(v_tile, t);
+      make_gates(gates, x, fixed, wave, lane, 16 * wave + m < (chunk + 1 < chunks ? 64 : tail), p.scale);
+      meet();  // the tiles are whole
+      if (chunk + 1 < chunks) fetch(chunk + 1);
+      by_wave(wave, [&](auto w) {
+        Scores<false, KD, decltype(w)::value> scores;
+        scores.read(q_tile, k_tile, gates, grp, m);
+        scores.make(p.log2_scale, grp, m);
+        scores.write(p_tile, lane);
+      });
+      meet();  // the tiles have been read, P is whole
+    }
+    return;
   }
 
-  for (int64_t at = 0; at < task.len; at += 64) {
-    const int left = static_cast<int>(task.len - at < 64 ? task.len - at : 64);
-    __syncthreads();  // the previous chunk's operands have been read
-    qt.store(q_tile, tid);
-    kt.store(k_tile, tid);
-    vt.store(v_tile, tid);
-    make_gates(gates, x, fixed, wave, lane, 16 * wave + m < left, p.scale);
-    __syncthreads();
-    if (at + 64 < task.len) fetch(at + 64);
-
-    by_wave(wave, [&](auto w) {
-      Scores<BF16, KD, decltype(w)::value> scores;
-      scores.read(q_tile, k_tile, gates, grp, m);
-      scores.make(p.log2_scale, grp, m);
-      scores.write(p_tile, lane);
-    });
-
+  const int row0 = task.vblk * R + wave * 16;  // the wave's first value row
+  f32x4 S[KD / 16];
+#pragma unroll
+  for (int t = 0; t < KD / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const StateAt from = start_state(p, task, KD), to = end_state(p, task, KD);
+  if (from.base) load_state_f32(S, from.base, from.at, from.bf16, row0 + m, grp);
+  for (int chunk = 0; chunk < chunks; ++chunk) {
+    meet();
     // O^T from the entering state.
     const BlockDecays bd = block_decays(gates);
-    f32x4 O[4][NC];
-    {
-      Frag sf[NC][KB];
+    f32x4 O[4];
 #pragma unroll
-      for (int c = 0; c < NC; ++c)
+    for (int it = 0; it < 4; ++it) O[it] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) to_frag(S[2 * kb][c], S[2 * kb + 1][c], sf[c][kb]);
+    for (int h = 0; h < KD / 64; ++h) {
+      f32x4 q[4][4];
 #pragma unroll
-      for (int it = 0; it < 4; ++it) {
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) O[it][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int it = 0; it < 4; ++it)
+          q[j][it] = *reinterpret_cast<const f32x4*>(q_tile + 16 * piece_at<kPprK>(16 * it + m, 16 * h + 4 * grp + j));
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) {
-          Frag qf;
-          row_frag<kPprK>(q_tile, 16 * it + m, kb, grp, qf);
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int c = 0; c < NC; ++c) O[it][c] = mma(sf[c][kb], qf, O[it][c]);
-        }
-        const float d = bd.before[it] * gates.a[16 * it + m];
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) O[it][c] *= d;
-      }
+          for (int it = 0; it < 4; ++it)
+            O[it] = __builtin_amdgcn_mfma_f32_16x16x4f32(S[4 * h + t][j], q[j][it][t], O[it], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    Frag vf[NC][2];
 #pragma unroll
-    for (int c = 0; c < NC; ++c)
+    for (int it = 0; it < 4; ++it) O[it] *= bd.before[it] * gates.a[16 * it + m];
+    F32x8 vf[2];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb)
-        col_frag<kPprV>(v_tile, wave * 16 * NC + 4 * c, 4 * NC, kb, grp, m, vf[c][kb]);
-    update_state<BF16, KD, NC, LOW>(S, vf, k_tile, gates, bd, grp, m);
-    __syncthreads();  // P is whole
+    for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[kb]);
+    update_state_f32<KD>(S, vf, k_tile, gates, bd, grp, m);
+    meet();
 
 #pragma unroll
-    for (int it = 0; it < 4; ++it) {
+    for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int kb = 0; kb <= it / 2; ++kb) {
-        Frag pf;
-        p_frag(p_tile, it, kb, 16 * lane, pf);
-#pragma unroll
-        for (int c = 0; c < NC; ++c) O[it][c] = mma(vf[c][kb], pf, O[it][c]);
+      for (int it = 2 * kb; it < 4; it += 2) {
+        F32x8 pf[2];
+        p_frag(p_tile, it, kb, 16 * lane, pf[0]);
+        p_frag(p_tile, it + 1, kb, 16 * lane, pf[1]);
+        mma_pair(vf[kb], pf, O[it], O[it + 1]);
       }
-    }
+    const int rows = chunk + 1 < chunks ? 64 : tail;
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
       const int i = 16 * it + m;
-      if (i >= left) continue;
-      const int64_t e = ((task.tok0 + at + i) * p.H + task.h) * p.V + row0 + 4 * NC * grp;
-      if constexpr (BF16 && NC == 2) {
-        *reinterpret_cast<bf16x8*>(static_cast<unsigned short*>(p.o) + e) = pack8(O[it][0], O[it][1]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) store4<BF16>(p.o, e + 4 * c, O[it][c]);
-      }
+      if (i < rows)
+        store4<false>(p.o, ((task.tok0 + 64 * static_cast<int64_t>(chunk) + i) * p.H + task.h) * p.V + row0 + 4 * grp, O[it]);
     }
   }
-
-  if (task.last && p.state_out) {
-    const int64_t slot = p.out_idx ? p.out_idx[task.n] : task.n;
-    if (slot >= 0 && slot < p.pool_slots)
-      store_state(S, p.state_out, slot * p.slot_pitch + head_state, p.st_bf16, KD, row0, grp, m);
-  }
+  if (to.base) store_state_f32(S, const_cast<void*>(to.base), to.at, to.bf16, row0 + m, grp);
 }
 
 // BF16 I/O: eight waves and one barrier per chunk. Behind the barrier of chunk c its tiles
@@ -271,7 +248,7 @@ __global__ __launch_bounds__(256) void linear_f32_kernel(LinParams p) {
 //   outputs of chunk c from the entering state, and update the state.
 constexpr int kStages = 3;
 
-template <int KD, int NC, bool LOW>
+template <int KD, int NC, int PARTS>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_ring_kernel(LinParams p) {
   constexpr int R = 64 * NC;
   constexpr int KB = KD / 32;
@@ -373,23 +350,13 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   }
 
   const int row0 = task.vblk * R + wave * 16 * NC;  // the wave's first value row
-  // Start state: the scan's, or the sequence's own.
   f32x4 S[KD / 16][NC];
-  const int64_t head_state = static_cast<int64_t>(task.h) * p.V * KD;
-  if (p.segmented && !(task.first && task.last)) {
-    load_state(S, p.scan_s, (static_cast<int64_t>(task.h) * p.slots + task.slot) * p.V * KD, false, KD,
-               row0, grp, m);
-  } else {
-    const int64_t slot = p.in_idx ? p.in_idx[task.n] : task.n;
-    if (p.state_in && slot >= 0 && slot < p.pool_slots) {
-      load_state(S, p.state_in, slot * p.slot_pitch + head_state, p.st_bf16, KD, row0, grp, m);
-    } else {
 #pragma unroll
-      for (int t = 0; t < KD / 16; ++t)
+  for (int t = 0; t < KD / 16; ++t)
 #pragma unroll
-        for (int c = 0; c < NC; ++c) S[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-  }
+    for (int c = 0; c < NC; ++c) S[t][c] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const StateAt from = start_state(p, task, KD);
+  if (from.base) load_state(S, from.base, from.at, from.bf16, KD, row0, grp, m);
   // Output rows: stores past a chunk's last token are dropped by the bounds (of the chunk
   // before the first one all are).
   const uint32_t opitch = static_cast<uint32_t>(p.H) * p.V * 2;
@@ -467,7 +434,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb) to_frag(S[2 * kb][c], S[2 * kb + 1][c], sf[c][kb]);
+      for (int kb = 0; kb < KB; ++kb) sf[c][kb] = pack8(S[2 * kb][c], S[2 * kb + 1][c]);
     with_scores();
     read_queries(2);
     __builtin_amdgcn_sched_barrier(0);
@@ -507,11 +474,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     inter(2);
     __builtin_amdgcn_sched_barrier(0);
     scale(0), scale(1);
-    bf16x8 vw[NC][2], vl[NC][2];
+    bf16x8 vw[NC][2][PARTS];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) scale_frag<LOW>(vf[c][kb], kd.w[kb][0], kd.w[kb][1], vw[c][kb], vl[c][kb]);
+      for (int c = 0; c < NC; ++c) scale_frag<PARTS>(vf[c][kb], kd.w[kb][0], kd.w[kb][1], vw[c][kb]);
     read_keys(2);
     read_keys(3);
     __builtin_amdgcn_sched_barrier(0);
@@ -526,14 +493,14 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int c = 0; c < NC; ++c) S[u][c] *= bd.all;
 #pragma unroll
-      for (int part = 0; part < (LOW ? 2 : 1); ++part)
+      for (int part = 0; part < PARTS; ++part)
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
           for (int u = t; u < t + 2; ++u)
 #pragma unroll
             for (int c = 0; c < NC; ++c)
-              S[u][c] = mma(kf[u][kb], part == 0 ? vw[c][kb] : vl[c][kb], S[u][c]);
+              S[u][c] = mma(kf[u][kb], vw[c][kb][part], S[u][c]);
       __builtin_amdgcn_sched_barrier(0);
     }
     scale(2), scale(3);
@@ -548,37 +515,36 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     store(tail);
   }
 
-  if (task.last && p.state_out) {
-    const int64_t slot = p.out_idx ? p.out_idx[task.n] : task.n;
-    if (slot >= 0 && slot < p.pool_slots)
-      store_state(S, p.state_out, slot * p.slot_pitch + head_state, p.st_bf16, KD, row0, grp, m);
-  }
+  const StateAt to = end_state(p, task, KD);
+  if (to.base) store_state(S, const_cast<void*>(to.base), to.at, to.bf16, KD, row0, grp, m);
 }
 
-template <int KD, int NC, bool LOW>
+template <int KD, int NC, int PARTS>
 hipError_t go_ring(const LinParams& p, hipStream_t stream) {
   constexpr int kLds = kStages * (256 * KD + 128 * 64 * NC) + 2 * kScoreBytes<true> + 2 * sizeof(Gates);
   static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
   const int64_t sub = static_cast<int64_t>(p.heads_per_task) * p.vblocks;
   const int64_t wgs = (p.tasks + 7) / 8 * 8 * sub;
-  hipLaunchKernelGGL((linear_ring_kernel<KD, NC, LOW>), dim3(static_cast<unsigned>(wgs)), dim3(512), kLds,
+  hipLaunchKernelGGL((linear_ring_kernel<KD, NC, PARTS>), dim3(static_cast<unsigned>(wgs)), dim3(512), kLds,
                      stream, p);
   return hipGetLastError();
 }
 
 template <int KD>
 hipError_t go_f32(const LinParams& p, hipStream_t stream) {
+  constexpr int kLds = 64 * 4 * (2 * KD + kLinRows) + kScoreBytes<false> + sizeof(Gates);
+  static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
   const int64_t sub = static_cast<int64_t>(p.heads_per_task) * p.vblocks;
   const int64_t wgs = (p.tasks + 7) / 8 * 8 * sub;
-  hipLaunchKernelGGL((linear_f32_kernel<KD>), dim3(static_cast<unsigned>(wgs)), dim3(256), 0, stream, p);
+  hipLaunchKernelGGL((linear_f32_kernel<KD>), dim3(static_cast<unsigned>(wgs)), dim3(512), kLds, stream, p);
   return hipGetLastError();
 }
 
 template <int KD>
 hipError_t go_k(const LinParams& p, bool bf16, int rows, hipStream_t stream) {
   if (!bf16) return go_f32<KD>(p, stream);
-  if (rows == 128) return go_ring<KD, 2, false>(p, stream);
-  return p.hi_lo ? go_ring<KD, 1, true>(p, stream) : go_ring<KD, 1, false>(p, stream);
+  if (rows == 128) return go_ring<KD, 2, 1>(p, stream);
+  return p.split ? go_ring<KD, 1, 3>(p, stream) : go_ring<KD, 1, 1>(p, stream);
 }
 
 }  // namespace

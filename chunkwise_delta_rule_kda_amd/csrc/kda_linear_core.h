@@ -55,6 +55,21 @@ __device__ __forceinline__ f32x4 mma(const F32x8& a, const F32x8& b, f32x4 c) {
   return c;
 }
 
+// Two products with one FP32 operand in common, a and b[0] / b[1]: their FP32 MFMAs in turn,
+// since each waits for the one before it on the same accumulator.
+__device__ __forceinline__ void mma_pair(const F32x8& a, const F32x8 (&b)[2], f32x4& c0, f32x4& c1) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    c0 = __builtin_amdgcn_mfma_f32_16x16x4f32(a.lo[e], b[0].lo[e], c0, 0, 0, 0);
+    c1 = __builtin_amdgcn_mfma_f32_16x16x4f32(a.lo[e], b[1].lo[e], c1, 0, 0, 0);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    c0 = __builtin_amdgcn_mfma_f32_16x16x4f32(a.hi[e], b[0].hi[e], c0, 0, 0, 0);
+    c1 = __builtin_amdgcn_mfma_f32_16x16x4f32(a.hi[e], b[1].hi[e], c1, 0, 0, 0);
+  }
+}
+
 // Piece p of row r of a tile is stored at p ^ piece_swap(r).
 template <int PPR>
 __device__ __forceinline__ int piece_swap(int r) {
@@ -62,9 +77,6 @@ __device__ __forceinline__ int piece_swap(int r) {
   const int q = (r >> 2) & 3, low = (((q ^ (q >> 1)) & 1) << 1) | (q >> 1);  // 0, 2, 3, 1
   return (PPR >= 16 ? (r & 3) << 2 : (r & 2) << 1) | low;
 }
-__device__ __forceinline__ void to_frag(f32x4 lo, f32x4 hi, bf16x8& f) { f = pack8(lo, hi); }
-__device__ __forceinline__ void to_frag(f32x4 lo, f32x4 hi, F32x8& f) { f = F32x8{lo, hi}; }
-
 // Index (in 16-byte pieces) of piece p of row r in a tile of PPR pieces per row.
 template <int PPR>
 __device__ __forceinline__ int piece_at(int r, int p) {
@@ -113,29 +125,28 @@ __device__ __forceinline__ void col_frag(const unsigned char* tile, int base, in
   }
 }
 
-// x scaled by one factor per token; with LOW also the part that rounding to BF16 leaves.
-template <bool LOW>
-__device__ __forceinline__ void scale_frag(bf16x8 x, f32x4 wlo, f32x4 whi, bf16x8& f, bf16x8& low) {
+// x scaled by one factor per token, as PARTS BF16 numbers: the product rounded, then twice
+// what the rounding left. One part (off by at most 2^-8 of a term) goes into BF16 states, whose
+// own rounding is as large; three (2^-24, FP32's own) into FP32 states, whose updates are then
+// products of BF16 keys and FP32 numbers. Two parts left FP32 states 2.2e-6 off over 2000
+// tokens, three 1.1e-7 (as FP32 arithmetic does), for 6 % of the call's time.
+template <int PARTS>
+__device__ __forceinline__ void scale_frag(bf16x8 x, f32x4 wlo, f32x4 whi, bf16x8 (&f)[PARTS]) {
   f32x4 lo, hi;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     lo[e] = static_cast<float>(x[e]) * wlo[e];
     hi[e] = static_cast<float>(x[4 + e]) * whi[e];
   }
-  f = pack8(lo, hi);
-  if constexpr (LOW) {
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    f[i] = pack8(lo, hi);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      lo[e] -= static_cast<float>(f[e]);
-      hi[e] -= static_cast<float>(f[4 + e]);
+      lo[e] -= static_cast<float>(f[i][e]);
+      hi[e] -= static_cast<float>(f[i][4 + e]);
     }
-    low = pack8(lo, hi);
   }
-}
-template <bool LOW>
-__device__ __forceinline__ void scale_frag(const F32x8& x, f32x4 wlo, f32x4 whi, F32x8& f, F32x8&) {
-  f.lo = x.lo * wlo;
-  f.hi = x.hi * whi;
 }
 
 // The decay factors of one chunk, in LDS, by its four 16-token blocks.
@@ -432,6 +443,29 @@ __device__ __forceinline__ void store_state(const f32x4 (&S)[KT][NC], void* base
   }
 }
 
+// The state a workgroup starts from: the scan's, or the sequence's own; and where the last
+// segment's goes.
+struct StateAt {
+  const void* base;  // null: zeros (nothing is written)
+  int64_t at;        // element of the head's first value row
+  bool bf16;
+};
+__device__ __forceinline__ StateAt start_state(const LinParams& p, const LinTask& task, int K) {
+  if (p.segmented && !(task.first && task.last))
+    return {p.scan_s, (static_cast<int64_t>(task.h) * p.slots + task.slot) * p.V * K, false};
+  const int64_t slot = p.in_idx ? p.in_idx[task.n] : task.n;
+  const bool held = p.state_in && slot >= 0 && slot < p.pool_slots;
+  return {held ? p.state_in : nullptr, slot * p.slot_pitch + static_cast<int64_t>(task.h) * p.V * K,
+          p.st_bf16 != 0};
+}
+__device__ __forceinline__ StateAt end_state(const LinParams& p, const LinTask& task, int K) {
+  if (!task.last || !p.state_out) return {nullptr, 0, false};
+  const int64_t slot = p.out_idx ? p.out_idx[task.n] : task.n;
+  const bool held = slot >= 0 && slot < p.pool_slots;
+  return {held ? p.state_out : nullptr, slot * p.slot_pitch + static_cast<int64_t>(task.h) * p.V * K,
+          p.st_bf16 != 0};
+}
+
 // The decays of a lane's tokens kappa(kb, grp, e) to the end of the chunk.
 struct KeyDecays {
   f32x4 w[2][2];
@@ -444,36 +478,67 @@ struct KeyDecays {
   }
 };
 
-// S <- D S + K^T (V w) for one chunk; vf: the wave's V operands, w a token's decay to the
-// end of the chunk.
-template <bool BF16, int KD, int NC, bool LOW>
-__device__ __forceinline__ void update_state(f32x4 (&S)[KD / 16][NC],
-                                             const typename FragOf<BF16>::type (&vf)[NC][2],
-                                             const unsigned char* k_tile, const Gates& gt,
-                                             const BlockDecays& bd, int grp, int m) {
-  typedef typename FragOf<BF16>::type Frag;
-  constexpr int kPpr = KD * (BF16 ? 2 : 4) / 16;
-  Frag vw[NC][2], vl[NC][2];
+// FP32 I/O. Key tile t of the state, rows r: key 64 (t / 4) + 4 r + t % 4, so that a 16-byte
+// read of four keys of a token is an operand of four tiles (4-byte reads of single keys were
+// four times as many). A lane's S[t][j] is key 64 (t / 4) + 16 grp + 4 j + t % 4.
+template <int KT>
+__device__ __forceinline__ f32x4 keys_of(const f32x4 (&S)[KT], int h, int j) {
+  return f32x4{S[4 * h][j], S[4 * h + 1][j], S[4 * h + 2][j], S[4 * h + 3][j]};
+}
+template <int KT>
+__device__ __forceinline__ void load_state_f32(f32x4 (&S)[KT], const void* base, int64_t at, bool bf16,
+                                               int row, int grp) {
+#pragma unroll
+  for (int h = 0; h < KT / 4; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t idx = at + static_cast<int64_t>(row) * 16 * KT + 64 * h + 16 * grp + 4 * j;
+      const f32x4 x = bf16 ? load4<true>(base, idx) : load4<false>(base, idx);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) S[4 * h + t][j] = x[t];
+    }
+}
+template <int KT>
+__device__ __forceinline__ void store_state_f32(const f32x4 (&S)[KT], void* base, int64_t at, bool bf16,
+                                                int row, int grp) {
+#pragma unroll
+  for (int h = 0; h < KT / 4; ++h)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t idx = at + static_cast<int64_t>(row) * 16 * KT + 64 * h + 16 * grp + 4 * j;
+      if (bf16) store4<true>(base, idx, keys_of(S, h, j));
+      else store4<false>(base, idx, keys_of(S, h, j));
+    }
+}
+
+// S <- D S + K^T (V w) for one chunk; vf: the wave's V operands, w a token's decay to the end
+// of the chunk.
+template <int KD>
+__device__ __forceinline__ void update_state_f32(f32x4 (&S)[KD / 16], const F32x8 (&vf)[2],
+                                                 const unsigned char* k_tile, const Gates& gt,
+                                                 const BlockDecays& bd, int grp, int m) {
+  constexpr int kPpr = KD / 4, KH = KD / 64;
   KeyDecays kd;
   kd.read(gt, bd, grp);
 #pragma unroll
-  for (int kb = 0; kb < 2; ++kb)
+  for (int t = 0; t < KD / 16; ++t) S[t] *= bd.all;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) scale_frag<LOW>(vf[c][kb], kd.w[kb][0], kd.w[kb][1], vw[c][kb], vl[c][kb]);
+  for (int i = 0; i < 4; ++i) {  // 16 tokens: a lane's 16 i + 4 grp + e
+    const f32x4 v = i % 2 ? vf[i / 2].hi : vf[i / 2].lo;
+    const f32x4 vw = v * kd.w[i / 2][i % 2];
+    f32x4 k[4][KH];
 #pragma unroll
-  for (int t = 0; t < KD / 16; ++t) {
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
-    for (int c = 0; c < NC; ++c) S[t][c] *= bd.all;
+      for (int h = 0; h < KH; ++h)
+        k[e][h] = *reinterpret_cast<const f32x4*>(k_tile + 16 * piece_at<kPpr>(16 * i + 4 * grp + e, 16 * h + m));
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-      Frag kf;
-      col_frag<kPpr>(k_tile, 32 * (t / 2) + 4 * (t % 2), 8, kb, grp, m, kf);
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) {
-        S[t][c] = mma(kf, vw[c][kb], S[t][c]);
-        if constexpr (LOW) S[t][c] = mma(kf, vl[c][kb], S[t][c]);
-      }
-    }
+      for (int t = 0; t < KD / 16; ++t)
+        S[t] = __builtin_amdgcn_mfma_f32_16x16x4f32(k[e][t / 4][t % 4], vw[e], S[t], 0, 0, 0);
+    // reads of the next tokens beside these products, not of all
+    if (i % 2) __builtin_amdgcn_sched_barrier(0);
   }
 }
 

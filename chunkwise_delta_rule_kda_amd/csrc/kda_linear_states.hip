@@ -30,9 +30,9 @@ __global__ __launch_bounds__(256, 2) void linear_states_f32_kernel(LinParams p) 
   const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * 4);
   const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * 4);
 
-  f32x4 S[KD / 16][1];
+  f32x4 S[KD / 16];
 #pragma unroll
-  for (int t = 0; t < KD / 16; ++t) S[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int t = 0; t < KD / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
   float total = 1.f;
 
   Tile<kPprK> kt;
@@ -55,15 +55,15 @@ __global__ __launch_bounds__(256, 2) void linear_states_f32_kernel(LinParams p) 
     make_gates(gates, x, fixed, wave, lane, 16 * wave + m < left, 1.f);
     __syncthreads();
     if (at + 64 < task.len) fetch(at + 64);
-    F32x8 vf[1][2];
+    F32x8 vf[2];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[0][kb]);
+    for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[kb]);
     const BlockDecays bd = block_decays(gates);
     total *= bd.all;
-    update_state<false, KD, 1, false>(S, vf, k_tile, gates, bd, grp, m);
+    update_state_f32<KD>(S, vf, k_tile, gates, bd, grp, m);
   }
   const int64_t slot = static_cast<int64_t>(task.h) * p.slots + task.slot;
-  store_state(S, p.scan_s, slot * p.V * KD, false, KD, row0, grp, m);
+  store_state_f32(S, p.scan_s, slot * p.V * KD, false, row0 + m, grp);
   if (tid == 0 && task.vblk == 0) p.scan_d[slot] = total;
 }
 
@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256, 2) void linear_states_f32_kernel(LinParams p) 
 // c + 1, four update the state.
 constexpr int kStages = 3;
 
-template <int KD, bool LOW>
+template <int KD, int PARTS>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 4))) void linear_states_kernel(LinParams p) {
   constexpr int R = kLinRows;
   constexpr int kPprK = KD / 8, kPprV = R / 8;
@@ -161,18 +161,17 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 4))) voi
       for (int kb = 0; kb < 2; ++kb) col_frag<kPprK>(k_tile, 32 * (t / 2) + 4 * (t % 2), 8, kb, grp, m, kf[t][kb]);
     __builtin_amdgcn_sched_barrier(0);
     total *= bd.all;
-    bf16x8 vw[2], vl[2];
+    bf16x8 vw[2][PARTS];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) scale_frag<LOW>(vf[0][kb], kd.w[kb][0], kd.w[kb][1], vw[kb], vl[kb]);
+    for (int kb = 0; kb < 2; ++kb) scale_frag<PARTS>(vf[0][kb], kd.w[kb][0], kd.w[kb][1], vw[kb]);
 #pragma unroll
-    for (int t = 0; t < KD / 16; ++t) {
-      S[t][0] *= bd.all;
+    for (int t = 0; t < KD / 16; ++t) S[t][0] *= bd.all;
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        S[t][0] = mma(kf[t][kb], vw[kb], S[t][0]);
-        if constexpr (LOW) S[t][0] = mma(kf[t][kb], vl[kb], S[t][0]);
-      }
-    }
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+        for (int t = 0; t < KD / 16; ++t) S[t][0] = mma(kf[t][kb], vw[kb][part], S[t][0]);
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   store_state(S, p.scan_s, slot * p.V * KD, false, KD, task.vblk * R + wave * 16, grp, m);
@@ -246,18 +245,18 @@ int64_t grid_of(const LinParams& p) {
   return (p.tasks + 7) / 8 * 8 * p.heads_per_task * p.vblocks;
 }
 
-template <int KD, bool LOW>
+template <int KD, int PARTS>
 hipError_t go(const LinParams& p, hipStream_t stream) {
   constexpr int kLds = kStages * 128 * (KD + kLinRows) + 2 * sizeof(Gates);
   static_assert(kLds <= 80 * 1024, "two workgroups per compute unit");
-  hipLaunchKernelGGL((linear_states_kernel<KD, LOW>), dim3(static_cast<unsigned>(grid_of(p))), dim3(512),
+  hipLaunchKernelGGL((linear_states_kernel<KD, PARTS>), dim3(static_cast<unsigned>(grid_of(p))), dim3(512),
                      kLds, stream, p);
   return hipGetLastError();
 }
 
 template <int KD>
 hipError_t go_k(const LinParams& p, bool bf16, hipStream_t stream) {
-  if (bf16) return p.hi_lo ? go<KD, true>(p, stream) : go<KD, false>(p, stream);
+  if (bf16) return p.split ? go<KD, 3>(p, stream) : go<KD, 1>(p, stream);
   hipLaunchKernelGGL((linear_states_f32_kernel<KD>), dim3(static_cast<unsigned>(grid_of(p))), dim3(256), 0,
                      stream, p);
   return hipGetLastError();

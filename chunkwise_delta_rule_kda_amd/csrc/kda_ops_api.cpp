@@ -131,18 +131,18 @@ LinPlan linear_plan(const kda_linear_args* a) {
   }
   // The chunked form's geometry: the cheapest by a model of the time, in microseconds, with
   // the costs of a 64-token step as measured on one MI355X (BF16 I/O, K = V = 128; FP32 I/O
-  // about five times that). A compute unit takes one workgroup at a time.
+  // 7 and 10.2). A compute unit takes one workgroup at a time.
   //   serial    6 + steps x 1.33 (64 value rows) or 1.85 (128) x rounds of 256 workgroups
-  //   segments 16 + steps of a segment x 2.7 (64) or 5 (128), both passes and the scan, at
-  //            as many segments as one round holds
-  // E.g. T = 8192: H = 6 37 us by 64-row segments, 170 serial; H = 48 148 us by 128-row
+  //   segments 10 + rounds x (6 + steps of a segment x 2.7 (64) or 5 (128)), both passes and
+  //            the scan, at as many segments as the rounds hold
+  // E.g. T = 8192: H = 6 33 us by 64-row segments, 170 serial; H = 48 136 us by 128-row
   // segments, 187 by 64-row ones, 228 serial; H = 96 248 us serial by 64 rows, 283 by 128,
   // 243 (two 128-row segments and a workspace). T = 1024: H = 6 22 us by segments, 25
-  // serial; H = 48 27 us serial, 35 by segments.
+  // serial; H = 48 27 us serial, 35 by segments. FP32 I/O, T = 1999, H = 48: 152 us by
+  // segments over two rounds, 177 over one, 228 serial.
   constexpr int64_t kUnits = 256;  // compute units
   const bool bf16 = a->io_dtype == KDA_BF16;
-  const double slow = bf16 ? 1.0 : 5.0;
-  // 128 rows of an FP32 state (its updates in two parts) do not fit the registers
+  // 128 rows of an FP32 state (its updates in three parts) do not fit the registers
   const int most = bf16 && a->state_dtype == KDA_BF16 && a->V % 128 == 0 ? 128 : 64;
   // a packed batch's longest sequence is taken for 1.75 times the mean
   const double steps = a->cu_seqlens && a->N > 1
@@ -152,20 +152,25 @@ LinPlan linear_plan(const kda_linear_args* a) {
   int64_t seg = 0;
   for (int rows = 64; rows <= most; rows *= 2) {
     const int64_t blocks = a->H * (a->V / rows), wgs = a->N * blocks;
-    const double serial = 6 + steps * (rows == 64 ? 1.33 : 1.85) * slow * static_cast<double>(ceil_div(wgs, kUnits));
+    const double serial = 6 + steps * (!bf16 ? 7.0 : rows == 64 ? 1.33 : 1.85) * static_cast<double>(ceil_div(wgs, kUnits));
     if (serial < best) {
       best = serial;
       pl.rows = rows;
       seg = 0;
     }
-    if (a->segment_tokens != 0 || wgs > kUnits / 2) continue;
-    int64_t len = a->cu_seqlens ? ceil_div(a->T * blocks, kUnits - wgs) : ceil_div(a->T, kUnits / wgs);
-    len = ceil_div(len < 128 ? 128 : len, kda::kLinChunk) * kda::kLinChunk;
-    const double cut = 16 + static_cast<double>(len / 64) * (rows == 64 ? 2.7 : 5.0) * slow;
-    if (len < a->T && cut < best) {
-      best = cut;
-      pl.rows = rows;
-      seg = len;
+    // FP32 I/O, bound by its products, also gains from segments over several rounds
+    for (int64_t rounds = 1; a->segment_tokens == 0 && rounds <= (bf16 ? 1 : 3); ++rounds) {
+      const int64_t units = kUnits * rounds;
+      if (wgs > units / 2) continue;
+      int64_t len = a->cu_seqlens ? ceil_div(a->T * blocks, units - wgs) : ceil_div(a->T, units / wgs);
+      len = ceil_div(len < 128 ? 128 : len, kda::kLinChunk) * kda::kLinChunk;
+      const double cut = 10 + static_cast<double>(rounds) *
+                                  (6 + static_cast<double>(len / 64) * (!bf16 ? 10.2 : rows == 64 ? 2.7 : 5.0));
+      if (len < a->T && cut < best) {
+        best = cut;
+        pl.rows = rows;
+        seg = len;
+      }
     }
   }
   if (a->segment_tokens > 0) seg = a->segment_tokens;
@@ -489,7 +494,7 @@ kda_status kda_linear(const kda_linear_args* a, void* stream_) {
   p.log2_scale = std::log2(static_cast<double>(p.scale));
   p.g_bf16 = a->g_dtype == KDA_BF16;
   p.st_bf16 = a->state_dtype == KDA_BF16;
-  p.hi_lo = bf16 && !p.st_bf16;
+  p.split = bf16 && !p.st_bf16;
   p.pool_slots = a->N;
   p.slot_pitch = a->H * a->V * a->K;
   if (a->ssm_state_indices) {

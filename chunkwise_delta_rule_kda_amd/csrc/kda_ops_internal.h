@@ -32,7 +32,7 @@ struct LinParams {
   float scale;
   double log2_scale;
   int32_t g_bf16, st_bf16;
-  int32_t hi_lo;             // FP32 states of BF16 inputs: the decayed values in two parts
+  int32_t split;             // FP32 states of BF16 inputs: the decayed values in three parts
   const int32_t* in_idx;     // pool slots read and written (null: sequence n at n)
   const int32_t* out_idx;
   int64_t pool_slots, slot_pitch;

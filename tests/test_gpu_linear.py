@@ -11,7 +11,7 @@ Tolerances, element by element. With a = the oracle's sum of absolute terms and 
   chunk sums 64 tokens and K keys, and each of the T / 64 chunks adds a decay (exp2 of a
   rounded exponent: below 2^-24 (2 + |x|) relative, and |x| 2^-x <= 0.54, so 3 2^-24 of the
   undecayed term) and a product: e = (K + 64 + 8 (T / 64 + 2)) 2^-24. The split values
-  leave below 2^-16 of a term each (two parts).
+  leave 2^-24 of a term (three parts of eight bits).
 """
 
 import numpy as np
@@ -104,7 +104,7 @@ def check(o, s, ref, d, name):
     if s is not None:
         bf16_state = s.dtype == torch.bfloat16
         own = U * np.abs(s_ref) if bf16_state else 0.0
-        term = U if bf16 and bf16_state else 2.0 ** -16 if bf16 else 0.0
+        term = U if bf16 and bf16_state else 2.0 ** -24 if bf16 else 0.0
         within(host(s), s_ref, own + (term + e) * s_abs, name + " state")
 
 
