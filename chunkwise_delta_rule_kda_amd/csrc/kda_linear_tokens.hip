@@ -126,17 +126,12 @@ template <bool BF16>
 hipError_t go_io(const LinParams& p, int k_dim, int rows, hipStream_t stream) {
   if (k_dim == 128) {
     switch (rows) {
-      case 128: return go<BF16, 128, 8>(p, stream);
       case 64: return go<BF16, 128, 4>(p, stream);
       case 32: return go<BF16, 128, 2>(p, stream);
       default: return go<BF16, 128, 1>(p, stream);
     }
   }
-  switch (rows) {
-    case 128: return go<BF16, 64, 4>(p, stream);
-    case 64: return go<BF16, 64, 2>(p, stream);
-    default: return go<BF16, 64, 1>(p, stream);
-  }
+  return rows == 64 ? go<BF16, 64, 2>(p, stream) : go<BF16, 64, 1>(p, stream);
 }
 
 }  // namespace

@@ -130,18 +130,22 @@ __global__ __launch_bounds__(256) void norm_narrow_kernel(NormParams p) {
   });
 }
 
-// D <= 2048 NV: a row is a workgroup.
-template <bool BF16, int NV>
-__global__ __launch_bounds__(256) void norm_wide_kernel(NormParams p) {
-  __shared__ float part[2][4];
+// D <= 8 THREADS NV: a row is a workgroup.
+template <bool BF16, int THREADS, int NV>
+__global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormParams p) {
+  constexpr int kWaves = THREADS / 64;
+  __shared__ float part[2][kWaves];
   int turn = 0;
-  norm_row<BF16, 256, NV>(p, blockIdx.x, threadIdx.x, [&](float x) {
+  norm_row<BF16, THREADS, NV>(p, blockIdx.x, threadIdx.x, [&](float x) {
 #pragma unroll
     for (int s = 1; s < 64; s <<= 1) x += __shfl_xor(x, s);
     float* w = part[turn++];  // the second sum has words of its own
     if ((threadIdx.x & 63) == 0) w[threadIdx.x >> 6] = x;
     __syncthreads();
-    return (w[0] + w[1]) + (w[2] + w[3]);
+    float all = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) all += w[i];
+    return all;
   });
 }
 
@@ -152,19 +156,20 @@ hipError_t go(const NormParams& p, hipStream_t stream) {
     const int64_t per = 256 / lanes;
     hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), 0, stream, p);
   };
-  auto wide = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, p);
+  auto wide = [&](auto kernel, int threads) {
+    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, stream, p);
   };
   if (p.D <= 64) narrow(norm_narrow_kernel<BF16, 8>, 8);
   else if (p.D <= 128) narrow(norm_narrow_kernel<BF16, 16>, 16);
   else if (p.D <= 256) narrow(norm_narrow_kernel<BF16, 32>, 32);
   else if (p.D <= 512) narrow(norm_narrow_kernel<BF16, 64>, 64);
-  else if (p.D <= 2048) wide(norm_wide_kernel<BF16, 1>);
-  else if (p.D <= 4096) wide(norm_wide_kernel<BF16, 2>);
-  else if (p.D <= 6144) wide(norm_wide_kernel<BF16, 3>);
-  else if (p.D <= 8192) wide(norm_wide_kernel<BF16, 4>);
-  else if (p.D <= 12288) wide(norm_wide_kernel<BF16, 6>);
-  else wide(norm_wide_kernel<BF16, 8>);
+  else if (p.D <= 1024) wide(norm_wide_kernel<BF16, 128, 1>, 128);
+  else if (p.D <= 2048) wide(norm_wide_kernel<BF16, 256, 1>, 256);
+  else if (p.D <= 4096) wide(norm_wide_kernel<BF16, 256, 2>, 256);
+  else if (p.D <= 6144) wide(norm_wide_kernel<BF16, 256, 3>, 256);
+  else if (p.D <= 8192) wide(norm_wide_kernel<BF16, 512, 2>, 512);
+  else if (p.D <= 12288) wide(norm_wide_kernel<BF16, 512, 3>, 512);
+  else wide(norm_wide_kernel<BF16, 512, 4>, 512);
   return hipGetLastError();
 }
 

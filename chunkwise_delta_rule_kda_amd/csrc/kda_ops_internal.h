@@ -56,7 +56,7 @@ hipError_t launch_linear_chunks(const LinParams& p, int k_dim, bool io_bf16, int
                                 hipStream_t stream);
 hipError_t launch_linear_states(const LinParams& p, int k_dim, bool io_bf16, hipStream_t stream);
 hipError_t launch_linear_scan(const LinParams& p, int k_dim, hipStream_t stream);
-// rows: state rows per workgroup (16 to 128)
+// rows: state rows per workgroup (16, 32 or 64; 32 or 64 with K = 64)
 hipError_t launch_linear_tokens(const LinParams& p, int k_dim, bool io_bf16, int rows,
                                 hipStream_t stream);
 
