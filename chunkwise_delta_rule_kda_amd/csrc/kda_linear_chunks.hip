@@ -523,8 +523,7 @@ template <int KD, int NC, int PARTS>
 hipError_t go_ring(const LinParams& p, hipStream_t stream) {
   constexpr int kLds = kStages * (256 * KD + 128 * 64 * NC) + 2 * kScoreBytes<true> + 2 * sizeof(Gates);
   static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
-  const int64_t sub = static_cast<int64_t>(p.heads_per_task) * p.vblocks;
-  const int64_t wgs = (p.tasks + 7) / 8 * 8 * sub;
+  const int64_t wgs = linear_grid(p);
   hipLaunchKernelGGL((linear_ring_kernel<KD, NC, PARTS>), dim3(static_cast<unsigned>(wgs)), dim3(512), kLds,
                      stream, p);
   return hipGetLastError();
@@ -534,8 +533,7 @@ template <int KD>
 hipError_t go_f32(const LinParams& p, hipStream_t stream) {
   constexpr int kLds = 64 * 4 * (2 * KD + kLinRows) + kScoreBytes<false> + sizeof(Gates);
   static_assert(kLds <= 160 * 1024, "LDS of a compute unit");
-  const int64_t sub = static_cast<int64_t>(p.heads_per_task) * p.vblocks;
-  const int64_t wgs = (p.tasks + 7) / 8 * 8 * sub;
+  const int64_t wgs = linear_grid(p);
   hipLaunchKernelGGL((linear_f32_kernel<KD>), dim3(static_cast<unsigned>(wgs)), dim3(512), kLds, stream, p);
   return hipGetLastError();
 }

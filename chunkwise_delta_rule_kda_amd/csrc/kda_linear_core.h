@@ -332,16 +332,17 @@ struct LinTask {
 };
 
 __device__ __forceinline__ bool find_task(const LinParams& p, LinTask& t) {
-  const int sub = p.heads_per_task * p.vblocks;
+  // Workgroup b runs on XCD b % 8. A task, one head of one slot, has its value blocks on one
+  // XCD, whose L2 then reads q and k once.
   const int64_t b = blockIdx.x;
-  const int64_t i = b >> 3;
-  const int64_t task = (i / sub) * 8 + (b & 7);
-  if (task >= p.tasks) return false;
-  const int s = static_cast<int>(i % sub);
-  const int groups = p.H / p.heads_per_task;
-  const int64_t w = task / groups;
-  t.h = static_cast<int>(task % groups) * p.heads_per_task + s / p.vblocks;
-  t.vblk = s % p.vblocks;
+  const int xcd = static_cast<int>(b & 7);
+  int64_t i = b >> 3;
+  t.vblk = static_cast<int>(i % p.vblocks);
+  i /= p.vblocks;
+  const int64_t task = i * 8 + xcd;
+  const int64_t w = task / p.H;
+  if (w >= p.slots) return false;
+  t.h = static_cast<int>(task % p.H);
   t.slot = w;
   int64_t begin, end, seg;
   if (p.longest_first) {

@@ -241,15 +241,11 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(LinParams p, int K) {
   }
 }
 
-int64_t grid_of(const LinParams& p) {
-  return (p.tasks + 7) / 8 * 8 * p.heads_per_task * p.vblocks;
-}
-
 template <int KD, int PARTS>
 hipError_t go(const LinParams& p, hipStream_t stream) {
   constexpr int kLds = kStages * 128 * (KD + kLinRows) + 2 * sizeof(Gates);
   static_assert(kLds <= 80 * 1024, "two workgroups per compute unit");
-  hipLaunchKernelGGL((linear_states_kernel<KD, PARTS>), dim3(static_cast<unsigned>(grid_of(p))), dim3(512),
+  hipLaunchKernelGGL((linear_states_kernel<KD, PARTS>), dim3(static_cast<unsigned>(linear_grid(p))), dim3(512),
                      kLds, stream, p);
   return hipGetLastError();
 }
@@ -257,7 +253,7 @@ hipError_t go(const LinParams& p, hipStream_t stream) {
 template <int KD>
 hipError_t go_k(const LinParams& p, bool bf16, hipStream_t stream) {
   if (bf16) return p.split ? go<KD, 3>(p, stream) : go<KD, 1>(p, stream);
-  hipLaunchKernelGGL((linear_states_f32_kernel<KD>), dim3(static_cast<unsigned>(grid_of(p))), dim3(256), 0,
+  hipLaunchKernelGGL((linear_states_f32_kernel<KD>), dim3(static_cast<unsigned>(linear_grid(p))), dim3(256), 0,
                      stream, p);
   return hipGetLastError();
 }

@@ -517,8 +517,6 @@ kda_status kda_linear(const kda_linear_args* a, void* stream_) {
   p.scan_s = static_cast<float*>(a->workspace);
   p.scan_d = reinterpret_cast<float*>(static_cast<unsigned char*>(a->workspace) + pl.scan_d);
   p.vblocks = static_cast<int32_t>(a->V / pl.rows);
-  p.heads_per_task = 1;
-  p.tasks = pl.slots * a->H;
   hipError_t e = hipSuccess;
   if (pl.seg) {
     kda::LinParams ps = p;

@@ -46,11 +46,11 @@ struct LinParams {
   int32_t longest_first;     // serial varlen form: workgroups by decreasing sequence length
   float* scan_s;             // FP32 [H][slots][V][K]
   float* scan_d;             // FP32 [H][slots]: the segment's total decay
-  // Grid: tasks of `sub` workgroups each (sub = heads per task * value blocks), a task's
-  // workgroups on one XCD.
-  int32_t vblocks, heads_per_task;
-  int64_t tasks;
+  int32_t vblocks;           // workgroups (value blocks) of one head of a slot
 };
+
+// Workgroups of a chunk launch (see find_task).
+inline int64_t linear_grid(const LinParams& p) { return (p.slots * p.H + 7) / 8 * 8 * p.vblocks; }
 
 hipError_t launch_linear_chunks(const LinParams& p, int k_dim, bool io_bf16, int rows,
                                 hipStream_t stream);
