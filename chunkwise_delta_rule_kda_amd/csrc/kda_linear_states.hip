@@ -7,76 +7,18 @@ namespace kda {
 
 namespace {
 
-// FP32 I/O: 64 value rows of one (segment, head); Z_p to the segment's scan slot, the
-// segment's total decay to scan_d.
-template <int KD>
-__global__ __launch_bounds__(256, 2) void linear_states_f32_kernel(LinParams p) {
-  constexpr int R = kLinRows;
-  constexpr int kPprK = KD / 4, kPprV = R / 4;
-  __shared__ __align__(16) unsigned char k_tile[64 * KD * 4];
-  __shared__ __align__(16) unsigned char v_tile[64 * R * 4];
-  __shared__ Gates gates;
-
-  LinTask task;
-  if (!find_task(p, task) || task.last) return;  // uniform
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
-  const int grp = lane >> 4, m = lane & 15;
-  const int hk = task.h / (p.H / p.Hk);
-  const int row0 = task.vblk * R + wave * 16;
-  const unsigned char* kp = static_cast<const unsigned char*>(p.k) +
-                            (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * 4;
-  const unsigned char* vp = static_cast<const unsigned char*>(p.v) +
-                            (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * 4;
-  const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * 4);
-  const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * 4);
-
-  f32x4 S[KD / 16];
-#pragma unroll
-  for (int t = 0; t < KD / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float total = 1.f;
-
-  Tile<kPprK> kt;
-  Tile<kPprV> vt;
-  const float fixed = p.log_decay ? p.log_decay[task.h] : 0.f;
-  float x = 0.f;
-  auto fetch = [&](int64_t at) {
-    const int left = static_cast<int>(task.len - at < 64 ? task.len - at : 64);
-    kt.load(kp + at * kpitch, kpitch, left, tid);
-    vt.load(vp + at * vpitch, vpitch, left, tid);
-    const int i = 16 * wave + m;
-    x = load_log_decay(p, task.tok0 + at + (i < left ? i : left - 1), task.h);
-  };
-  if (task.len > 0) fetch(0);
-  for (int64_t at = 0; at < task.len; at += 64) {
-    const int left = static_cast<int>(task.len - at < 64 ? task.len - at : 64);
-    __syncthreads();
-    kt.store(k_tile, tid);
-    vt.store(v_tile, tid);
-    make_gates(gates, x, fixed, wave, lane, 16 * wave + m < left, 1.f);
-    __syncthreads();
-    if (at + 64 < task.len) fetch(at + 64);
-    F32x8 vf[2];
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[kb]);
-    const BlockDecays bd = block_decays(gates);
-    total *= bd.all;
-    update_state_f32<KD>(S, vf, k_tile, gates, bd, grp, m);
-  }
-  const int64_t slot = static_cast<int64_t>(task.h) * p.slots + task.slot;
-  store_state_f32(S, p.scan_s, slot * p.V * KD, false, row0 + m, grp);
-  if (tid == 0 && task.vblk == 0) p.scan_d[slot] = total;
-}
-
-// BF16 I/O: the same by eight waves as in the output launch (kda_linear_chunks.hip): four
-// load the tiles of chunk c + 2 into a ring of three and make the decay factors of chunk
-// c + 1, four update the state.
+// 64 value rows of one (segment, head) by eight waves, as in the output launch
+// (kda_linear_chunks.hip): four load the tiles of chunk c + 2 into a ring of three and make
+// the decay factors of chunk c + 1, four update the state. Z_p goes to the segment's scan
+// slot, the segment's total decay to scan_d.
 constexpr int kStages = 3;
 
-template <int KD, int PARTS>
+template <bool BF16, int KD, int PARTS>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 4))) void linear_states_kernel(LinParams p) {
   constexpr int R = kLinRows;
-  constexpr int kPprK = KD / 8, kPprV = R / 8;
-  constexpr int kTileK = 128 * KD, kStage = kTileK + 128 * R;
+  constexpr int kElem = BF16 ? 2 : 4;
+  constexpr int kPprK = KD * kElem / 16, kPprV = R * kElem / 16;
+  constexpr int kTileK = 64 * KD * kElem, kStage = kTileK + 64 * R * kElem;
   constexpr int kLoads = AsyncTile<kPprK>::kLoads + AsyncTile<kPprV>::kLoads;
   extern __shared__ __align__(1024) unsigned char lds[];
   Gates* const gates = reinterpret_cast<Gates*>(lds + kStages * kStage);
@@ -93,11 +35,11 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 4))) voi
     __builtin_amdgcn_s_setprio(2);
     const int hk = task.h / (p.H / p.Hk);
     const unsigned char* kp = static_cast<const unsigned char*>(p.k) +
-                              (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * 2;
+                              (row_offset(p, p.ks, task.n, task.tok0) + hk * p.ks[2]) * kElem;
     const unsigned char* vp = static_cast<const unsigned char*>(p.v) +
-                              (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * 2;
-    const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * 2);
-    const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * 2);
+                              (row_offset(p, p.vs, task.n, task.tok0) + task.h * p.vs[2] + task.vblk * R) * kElem;
+    const uint32_t kpitch = static_cast<uint32_t>(p.ks[1] * kElem);
+    const uint32_t vpitch = static_cast<uint32_t>(p.vs[1] * kElem);
     AsyncTile<kPprK> kt;
     AsyncTile<kPprV> vt;
     kt.init(wave, lane, kpitch);
@@ -138,43 +80,61 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 4))) voi
     return;
   }
 
-  f32x4 S[KD / 16][1];
-#pragma unroll
-  for (int t = 0; t < KD / 16; ++t) S[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
   float total = 1.f;
   int stage = 0;
-  for (int chunk = 0; chunk < chunks; ++chunk) {
-    meet();
-    const unsigned char* k_tile = lds + stage * kStage;
-    const unsigned char* v_tile = k_tile + kTileK;
-    const Gates& gt = gates[chunk & 1];
-    bf16x8 vf[1][2], kf[KD / 16][2];
+  auto chunk_loop = [&](auto update) {
+    for (int chunk = 0; chunk < chunks; ++chunk) {
+      meet();
+      const unsigned char* k_tile = lds + stage * kStage;
+      const Gates& gt = gates[chunk & 1];
+      const BlockDecays bd = block_decays(gt);
+      update(k_tile, k_tile + kTileK, gt, bd);
+      total *= bd.all;
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+  };
+  const int row0 = task.vblk * R + wave * 16;
+  if constexpr (BF16) {
+    f32x4 S[KD / 16][1];
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[0][kb]);
-    const BlockDecays bd = block_decays(gt);
-    KeyDecays kd;
-    kd.read(gt, bd, grp);
-    // all reads before the products: left alone, each is read right before its use
+    for (int t = 0; t < KD / 16; ++t) S[t][0] = f32x4{0.f, 0.f, 0.f, 0.f};
+    chunk_loop([&](const unsigned char* k_tile, const unsigned char* v_tile, const Gates& gt, const BlockDecays& bd) {
+      bf16x8 vf[2], kf[KD / 16][2];
 #pragma unroll
-    for (int t = 0; t < KD / 16; ++t)
+      for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[kb]);
+      KeyDecays kd;
+      kd.read(gt, bd, grp);
+      // all reads before the products: left alone, each is read right before its use
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) col_frag<kPprK>(k_tile, 32 * (t / 2) + 4 * (t % 2), 8, kb, grp, m, kf[t][kb]);
-    __builtin_amdgcn_sched_barrier(0);
-    total *= bd.all;
-    bf16x8 vw[2][PARTS];
+      for (int t = 0; t < KD / 16; ++t)
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb) scale_frag<PARTS>(vf[0][kb], kd.w[kb][0], kd.w[kb][1], vw[kb]);
+        for (int kb = 0; kb < 2; ++kb) col_frag<kPprK>(k_tile, 32 * (t / 2) + 4 * (t % 2), 8, kb, grp, m, kf[t][kb]);
+      __builtin_amdgcn_sched_barrier(0);
+      bf16x8 vw[2][PARTS];
 #pragma unroll
-    for (int t = 0; t < KD / 16; ++t) S[t][0] *= bd.all;
+      for (int kb = 0; kb < 2; ++kb) scale_frag<PARTS>(vf[kb], kd.w[kb][0], kd.w[kb][1], vw[kb]);
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+      for (int t = 0; t < KD / 16; ++t) S[t][0] *= bd.all;
 #pragma unroll
-      for (int part = 0; part < PARTS; ++part)
+      for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-        for (int t = 0; t < KD / 16; ++t) S[t][0] = mma(kf[t][kb], vw[kb][part], S[t][0]);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+          for (int t = 0; t < KD / 16; ++t) S[t][0] = mma(kf[t][kb], vw[kb][part], S[t][0]);
+    });
+    store_state(S, p.scan_s, slot * p.V * KD, false, KD, row0, grp, m);
+  } else {
+    f32x4 S[KD / 16];
+#pragma unroll
+    for (int t = 0; t < KD / 16; ++t) S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    chunk_loop([&](const unsigned char* k_tile, const unsigned char* v_tile, const Gates& gt, const BlockDecays& bd) {
+      F32x8 vf[2];
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) col_frag<kPprV>(v_tile, wave * 16, 4, kb, grp, m, vf[kb]);
+      update_state_f32<KD>(S, vf, k_tile, gt, bd, grp, m);
+    });
+    store_state_f32(S, p.scan_s, slot * p.V * KD, false, row0 + m, grp);
   }
-  store_state(S, p.scan_s, slot * p.V * KD, false, KD, task.vblk * R + wave * 16, grp, m);
   if (tid == 0 && task.vblk == 0) p.scan_d[slot] = total;
 }
 
@@ -241,21 +201,19 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(LinParams p, int K) {
   }
 }
 
-template <int KD, int PARTS>
+template <bool BF16, int KD, int PARTS>
 hipError_t go(const LinParams& p, hipStream_t stream) {
-  constexpr int kLds = kStages * 128 * (KD + kLinRows) + 2 * sizeof(Gates);
-  static_assert(kLds <= 80 * 1024, "two workgroups per compute unit");
-  hipLaunchKernelGGL((linear_states_kernel<KD, PARTS>), dim3(static_cast<unsigned>(linear_grid(p))), dim3(512),
-                     kLds, stream, p);
+  constexpr int kLds = kStages * 64 * (BF16 ? 2 : 4) * (KD + kLinRows) + 2 * sizeof(Gates);
+  static_assert(kLds <= (BF16 ? 80 : 160) * 1024, "two workgroups (FP32: one) per compute unit");
+  hipLaunchKernelGGL((linear_states_kernel<BF16, KD, PARTS>), dim3(static_cast<unsigned>(linear_grid(p))),
+                     dim3(512), kLds, stream, p);
   return hipGetLastError();
 }
 
 template <int KD>
 hipError_t go_k(const LinParams& p, bool bf16, hipStream_t stream) {
-  if (bf16) return p.split ? go<KD, 3>(p, stream) : go<KD, 1>(p, stream);
-  hipLaunchKernelGGL((linear_states_f32_kernel<KD>), dim3(static_cast<unsigned>(linear_grid(p))), dim3(256), 0,
-                     stream, p);
-  return hipGetLastError();
+  if (!bf16) return go<false, KD, 1>(p, stream);
+  return p.split ? go<true, KD, 3>(p, stream) : go<true, KD, 1>(p, stream);
 }
 
 }  // namespace
