@@ -27,7 +27,7 @@ kda_status fail(kda_status s, const char* fmt, ...) {
 kda_status clear() { return kda::set_error(KDA_OK, ""); }
 
 constexpr int64_t kBig = int64_t(1) << 40;  // bound on sizes, strides and pitches
-constexpr int64_t kMaxGrid = 0x7fffffffLL;
+constexpr int64_t kMaxThreads = 0xffffffffLL;  // of one launch: HIP refuses more
 
 bool known_dtype(int32_t d) { return d == KDA_BF16 || d == KDA_FP32; }
 int64_t elem_size(int32_t d) { return d == KDA_BF16 ? 2 : 4; }
@@ -65,7 +65,7 @@ kda_status linear_shape(const kda_linear_args* a) {
       a->N > (int64_t(1) << 31))
     return fail(KDA_ERR_SHAPE, "bad B=%lld T=%lld N=%lld", (long long)a->B, (long long)a->T,
                 (long long)a->N);
-  if (a->H < 1 || a->H * a->V > (1 << 22))  // a chunk's rows of o stay within 2^31 bytes
+  if (a->H < 1 || a->H > (1 << 22) || a->H * a->V > (1 << 22))  // a chunk's rows of o stay within 2^31 bytes
     return fail(KDA_ERR_SHAPE, "H=%lld is not positive, or H*V exceeds 2^22", (long long)a->H);
   if (a->Hk < 1 || a->Hk > a->H || a->H % a->Hk)
     return fail(KDA_ERR_SHAPE, "Hk=%lld does not divide H=%lld", (long long)a->Hk, (long long)a->H);
@@ -204,9 +204,12 @@ kda_status linear_sizes(const kda_linear_args* a, LinPlan* out) {
   if ((tokens / kda::kLinChunk + a->N) * a->H * a->V * a->K > (Wide(1) << 56))
     return fail(KDA_ERR_SHAPE, "too many chunks");
   const LinPlan pl = linear_plan(a);
-  if (static_cast<Wide>(pl.tokens ? a->N : pl.slots + 8) * a->H * (a->V / 16) > kMaxGrid ||
-      static_cast<Wide>(a->N) * a->H * ceil_div(a->V * a->K, 1024) > kMaxGrid)
-    return fail(KDA_ERR_SHAPE, "too many workgroups (N*H, or segments*H)");
+  // the token loop's launch, or the scan's and the chunks'
+  const Wide pairs = static_cast<Wide>(a->N) * a->H;
+  const Wide threads = pl.tokens ? pairs * (a->V / pl.rows) * 256
+                                 : (static_cast<Wide>(pl.slots) * a->H + 8) * (a->V / pl.rows) * 512;
+  if (threads > kMaxThreads || (pl.seg && pairs * ceil_div(a->V * a->K, 1024) * 256 > kMaxThreads))
+    return fail(KDA_ERR_SHAPE, "too much for one launch (N*H, or segments*H)");
   *out = pl;
   return KDA_OK;
 }
@@ -311,8 +314,8 @@ bool same_pool(const kda_pool* a, const kda_pool* b) {
 constexpr int64_t kCopyGroup = 8192;  // elements of a slot per workgroup
 
 kda_status grid_of(const kda_pool* p, int64_t pairs) {
-  if (static_cast<Wide>(ceil_div(p->slot_elems, kCopyGroup)) * p->layers * pairs > kMaxGrid)
-    return fail(KDA_ERR_SHAPE, "too many pairs x layers x slot_elems");
+  if (static_cast<Wide>(ceil_div(p->slot_elems, kCopyGroup)) * p->layers * pairs * 256 > kMaxThreads)
+    return fail(KDA_ERR_SHAPE, "pairs x layers x slot_elems are too many for one launch");
   return KDA_OK;
 }
 
@@ -381,13 +384,20 @@ kda_status compact_check(const kda_pool_compact_args* a) {
 
 // ------------------------------------------------------------ gated norm
 
+// Threads of a row's workgroup or part of a wave (kda_norm.hip).
+int64_t norm_threads(int64_t D) {
+  int64_t t = 8;
+  while (t < 256 && 8 * t < D) t *= 2;
+  return D <= 6144 ? t : 512;
+}
+
 kda_status norm_check(const kda_gated_norm_args* a) {
   if (!a) return fail(KDA_ERR_NULL, "args is NULL");
   if (a->D < 8 || a->D > 16384 || a->D % 8)
     return fail(KDA_ERR_SHAPE, "D=%lld is not a multiple of 8 up to 16384", (long long)a->D);
   if (a->M < 0 || a->M > kBig || a->G < 1 || a->G > kBig ||
-      static_cast<Wide>(a->M) * a->G > kMaxGrid)
-    return fail(KDA_ERR_SHAPE, "M=%lld G=%lld", (long long)a->M, (long long)a->G);
+      static_cast<Wide>(a->M) * a->G * norm_threads(a->D) > kMaxThreads - 256)
+    return fail(KDA_ERR_SHAPE, "M=%lld G=%lld D=%lld", (long long)a->M, (long long)a->G, (long long)a->D);
   if (!known_dtype(a->io_dtype)) return fail(KDA_ERR_DTYPE, "io_dtype %d", a->io_dtype);
   if (a->act != KDA_ACT_SIGMOID && a->act != KDA_ACT_SILU)
     return fail(KDA_ERR_FLAGS, "act %d", a->act);

@@ -414,7 +414,8 @@ typedef struct kda_linear_args {
   size_t workspace_bytes;
 
   int64_t B, T, H, Hk, K, V, N; /* Hk divides H; K is 64 or 128; V a multiple of 64 up
-                                   to 512; N = number of sequences */
+                                   to 512; N = number of sequences; H * V at most 2^22,
+                                   T at most 2^36 */
   /* Strides in elements: batch, token, head. Not negative, multiples of 8 (0 repeats a
      row), a token stride of at most 2^22. */
   int64_t q_stride[3], k_stride[3], v_stride[3];

@@ -105,6 +105,23 @@ def test_linear_null_and_launch_refuse_before_any_launch():
     assert lib.kda_gated_norm(None, None) == 1
 
 
+def test_sizes_past_one_launch_are_refused():
+    # H * V wraps to 0 in 64 bits; a launch of 2^32 threads is past what HIP takes
+    assert status(H=1 << 57) == 2 and status(H=(1 << 22) + 1) == 2
+    tokens = dict(T=1, H=16, io_dtype=1, state_dtype=1, g=None, log_decay=None, state_in=None,
+                  state_out=None, workspace=None, workspace_bytes=0, q=at(0), k=at(200),
+                  v=at(400), o=at(900))
+    assert status(B=(1 << 17) - 1, **tokens) == 0      # 8 workgroups of 256 threads per head
+    assert status(B=1 << 17, **tokens) == 2
+    wide = dict(x=at(0), out=at(200), gate=None, res=None, w=None, nw=None, nxt=None, G=1,
+                D=16384, xs=(16384, 16384))
+    assert norm(M=(1 << 22) - 1, **wide) == 0 and norm(M=(1 << 23), **wide) == 2
+    narrow = dict(wide, D=64, xs=(64, 64))
+    assert norm(M=(1 << 29) - 64, **narrow) == 0 and norm(M=1 << 29, **narrow) == 2
+    assert copy(src=pool(slots=1 << 25, elems=8), dst=pool(9, slots=1 << 25, elems=8),
+                si=at(20), di=at(21), pairs=1 << 24) == 2
+
+
 def test_linear_plan():
     plan = lambda **kw: kda.kda_linear_plan(lin(**kw))
     for T in (1, 8):
