@@ -132,19 +132,26 @@ LinPlan linear_plan(const kda_linear_args* a) {
     pl.segs = 1;
     return pl;
   }
-  // The chunked form's geometry: the cheapest by a model of the time, in microseconds, with
-  // the costs of a 64-token step as measured on one MI355X (BF16 I/O, K = V = 128; FP32 I/O
-  // 7 and 10.2). A compute unit takes one workgroup at a time.
-  //   serial    6 + steps x 1.33 (64 value rows) or 1.85 (128) x rounds of 256 workgroups
-  //   segments 10 + rounds x (6 + steps of a segment x 2.7 (64) or 5 (128)), both passes and
-  //            the scan, at as many segments as the rounds hold
-  // E.g. T = 8192: H = 6 33 us by 64-row segments, 170 serial; H = 48 136 us by 128-row
-  // segments, 187 by 64-row ones, 228 serial; H = 96 248 us serial by 64 rows, 283 by 128,
-  // 243 (two 128-row segments and a workspace). T = 1024: H = 6 22 us by segments, 25
-  // serial; H = 48 27 us serial, 35 by segments. FP32 I/O, T = 1999, H = 48: 152 us by
-  // segments over two rounds, 177 over one, 228 serial.
+  // The chunked form's geometry: the cheapest by a model of the time, in microseconds, fitted
+  // to one MI355X (K = V = 128), where a compute unit takes one workgroup at a time and a step
+  // is 64 tokens. BF16 I/O, by 64 or 128 value rows, W workgroups (at most 256):
+  //   serial    5 + steps x 1.27 or 1.85 x rounds of 256 workgroups; a step takes 0.3 more
+  //             where q, k, v and o are more than the 256 MB of the last-level cache
+  //   segments  14.3 + 0.028 W + steps of a segment x 1.8, or 18 + 0.028 W + 3.5 x steps, both
+  //             passes and the scan; 2.7 and 4.5 a step past the last-level cache, from which
+  //             the second pass else reads k and v
+  // T = 8192: H = 6 32 us by 64-row segments, 168 serial; H = 12 44 by 64-row segments, 49 by
+  // 128-row ones; H = 40 (past the cache) 132 and 113, 220 serial; H = 96 239 to 248 serial, 283
+  // by 128 rows, 243 by two 128-row segments and a workspace. T = 1024: H = 6 21 us by segments,
+  // 24 serial; H = 20 27 and 25.
+  // FP32 I/O: serial 6 + 7 x steps x rounds, segments 10 + rounds x (6 + 10.2 x steps), bound
+  // by its products, so segments over several rounds gain as well: T = 1999, H = 48: 152 us
+  // over two rounds, 177 over one, 228 serial.
   constexpr int64_t kUnits = 256;  // compute units
   const bool bf16 = a->io_dtype == KDA_BF16;
+  const double bytes = static_cast<double>(elem_size(a->io_dtype)) * static_cast<double>(a->B) *
+                       static_cast<double>(a->T) * 2.0 * static_cast<double>(a->Hk * a->K + a->H * a->V);
+  const bool cached = bytes <= 256e6;
   // 128 rows of an FP32 state (its updates in three parts) do not fit the registers
   const int most = bf16 && a->state_dtype == KDA_BF16 && a->V % 128 == 0 ? 128 : 64;
   // a packed batch's longest sequence is taken for 1.75 times the mean
@@ -155,20 +162,24 @@ LinPlan linear_plan(const kda_linear_args* a) {
   int64_t seg = 0;
   for (int rows = 64; rows <= most; rows *= 2) {
     const int64_t blocks = a->H * (a->V / rows), wgs = a->N * blocks;
-    const double serial = 6 + steps * (!bf16 ? 7.0 : rows == 64 ? 1.33 : 1.85) * static_cast<double>(ceil_div(wgs, kUnits));
+    const double step = !bf16 ? 7.0 : (rows == 64 ? 1.27 : 1.85) + (cached ? 0.0 : 0.3);
+    const double serial = (bf16 ? 5 : 6) + steps * step * static_cast<double>(ceil_div(wgs, kUnits));
     if (serial < best) {
       best = serial;
       pl.rows = rows;
       seg = 0;
     }
-    // FP32 I/O, bound by its products, also gains from segments over several rounds
     for (int64_t rounds = 1; a->segment_tokens == 0 && rounds <= (bf16 ? 1 : 3); ++rounds) {
       const int64_t units = kUnits * rounds;
       if (wgs > units / 2) continue;
       int64_t len = a->cu_seqlens ? ceil_div(a->T * blocks, units - wgs) : ceil_div(a->T, units / wgs);
       len = ceil_div(len < 128 ? 128 : len, kda::kLinChunk) * kda::kLinChunk;
-      const double cut = 10 + static_cast<double>(rounds) *
-                                  (6 + static_cast<double>(len / 64) * (!bf16 ? 10.2 : rows == 64 ? 2.7 : 5.0));
+      const double chunks = static_cast<double>(len / 64);
+      const double filled = std::fmin(256.0, static_cast<double>(ceil_div(a->T, len) * wgs));
+      // three launches and a workspace have to save 5 %
+      const double cut = 1.05 * (!bf16 ? 10 + static_cast<double>(rounds) * (6 + 10.2 * chunks)
+                                 : rows == 64 ? 14.3 + 0.028 * filled + (cached ? 1.8 : 2.7) * chunks
+                                              : 18 + 0.028 * filled + (cached ? 3.5 : 4.5) * chunks);
       if (len < a->T && cut < best) {
         best = cut;
         pl.rows = rows;
