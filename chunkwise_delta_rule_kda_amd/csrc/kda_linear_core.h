@@ -8,23 +8,26 @@
 // passes 1 where the decays do not. The prefix sums are kept in FP64: their differences
 // are then exact to FP32 also behind a token that empties the state (-inf).
 //
-// One workgroup of four waves owns R = 64 NC value rows of one (segment, head) and walks
-// its chunks; each wave owns 16 NC of them with all keys, as MFMA accumulators
-// S[key][value] in registers, FP32. Everything is computed transposed (values or keys as
-// MFMA rows, tokens as columns), which lets the accumulators serve as operands without
-// any exchange between lanes:
+// One workgroup owns R = 64 NC value rows of one (segment, head) and walks its chunks with
+// eight waves: four that load tiles and form the scores P, and four "state waves" that each
+// own 16 NC of the rows with all keys, as MFMA accumulators S[key][value] in registers,
+// FP32. Everything is computed transposed (values or keys as MFMA rows, tokens as columns),
+// which lets the accumulators serve as operands without any exchange between lanes:
 //   P^T tile (j, i)     = K . Q^T, scaled by its decays, through LDS to all waves
 //   O^T tile (value, i) = S^T Q^T (scaled by s exp(G_i)) + V^T P^T
 //   S tile (key, value) = exp(G_C) S + K^T (V exp(G_C - G_j))
 // Two 16-key accumulator tiles hold keys 8 grp .. 8 grp + 7 of 32 in each lane (the K^T
-// operand's rows are permuted so), which are those of a plain 16-byte read of Q. For the contractions over tokens both sides use the order
+// operand's rows are permuted so), which are those of a plain 16-byte read of Q. For the
+// contractions over tokens both sides use the order
 // kappa(kb, grp, e) = 32 kb + 16 (e / 4) + 4 grp + e % 4.
 //
 // LDS tiles are rows of 16-byte pieces, permuted within a row by an exclusive or with a
 // number of the row's: one that differs over the 16 rows of a plain operand read, and in
 // its upper bits over the four rows from which 16 lanes of a transposing read take 32 or
-// 64 bytes each, so that both touch every bank alike. BF16 operands that need eight tokens of one column come from the transposing LDS
-// read; FP32 ones (FP32 I/O) from 4-byte reads.
+// 64 bytes each, so that both touch every bank alike. BF16 operands that need eight tokens
+// of one column come from the transposing LDS read; FP32 ones (FP32 I/O) from 4-byte reads.
+// Roundings to BF16 of BF16 calls: the state as the operand of S^T Q^T, the scores P and the
+// decayed values (see scale_frag), each by at most 2^-8 of a term; sums stay in FP32.
 #pragma once
 
 #include "kda_device.h"

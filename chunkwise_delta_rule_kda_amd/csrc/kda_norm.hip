@@ -2,7 +2,11 @@
 //   y = residual + scale * act(gate) * weight * x / sqrt(mean(x^2) + eps)
 //   z = next_weight * y / sqrt(mean(y^2) + eps)
 // A row is held in registers between its two reductions, so every tensor is read or
-// written once; the launch is bound by those bytes.
+// written once; the launch is bound by those bytes: 8192 x 12288 BF16 with gate, residual
+// and the next norm, 1007 MB in 182 us (5.5 TB/s); 8192 x 96 heads of 128 with a gate
+// 111 us (5.4 TB/s). Rows of at most 512 elements share a wave; wider ones are a workgroup
+// of as many threads as keep at most three or four pieces of eight each (2048 x 16384: 37 us
+// by 512 threads, 50 by 256 with twice the registers).
 
 #include "kda_device.h"
 #include "kda_ops_internal.h"

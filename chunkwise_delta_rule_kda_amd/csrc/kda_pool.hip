@@ -9,7 +9,10 @@ namespace kda {
 namespace {
 
 // A workgroup copies 256 x kUnits x 8 consecutive elements of one slot of one layer, all
-// loads before the first store.
+// loads before the first store. Bound by its bytes: 48 slots of 24 heads in four layers from
+// FP32 to BF16, 434 MB, 90 us (4.8 TB/s); 120 slots x 24 heads x two layers of FP32,
+// 755 MB, 146 us (5.2 TB/s). Pairs are known on the device only, so a compaction launches a
+// grid for the most moves there can be; a workgroup without one ends at once.
 constexpr int kUnits = 4;
 constexpr int kPerGroup = 256 * kUnits * 8;
 
@@ -62,7 +65,8 @@ constexpr int kWords = KDA_POOL_COMPACT_SLOTS / 32;
 
 // One workgroup: a bitmap of the live slots and its running counts in LDS. rank(s) is the
 // number of live slots below s; with L live ones in all, the free slot s < L is hole
-// number s - rank(s), and the live slot s >= L is move number rank(s) - rank(L).
+// number s - rank(s), and the live slot s >= L is move number rank(s) - rank(L). Bound by
+// the latency of its few passes: 2.6 us for 64 slots, 3.7 for 512.
 __global__ __launch_bounds__(1024) void pool_plan_kernel(const int32_t* idx, int32_t* new_idx,
                                                          int32_t* count, int64_t n, int slots,
                                                          int32_t* move_src, int32_t* move_dst,

@@ -39,7 +39,13 @@
  * precomputed g outside [-5, 0]) are undefined behaviour, as on the flashinfer page;
  * kda_debug_check_cu_seqlens is the explicit (synchronising) checker for tests.
  *
- * Indexing is 64-bit throughout: there is no 2^31 extent limit.
+ * Indexing is 64-bit throughout: there is no 2^31 extent limit. A call that would need a
+ * launch of 2^32 threads is refused.
+ *
+ * Beside kda_prefill, under the same rules of ownership, errors and indexing: kda_linear
+ * (linear attention with one decay per head), kda_pool_copy and kda_pool_compact (slots of
+ * a state pool) and kda_gated_norm (the norm behind an attention output or between two
+ * blocks); see their sections below.
  */
 #ifndef KDA_H
 #define KDA_H
