@@ -123,7 +123,7 @@ LinPlan linear_plan(const kda_linear_args* a) {
     pl.tokens = true;
     // 64 rows per workgroup where that gives 512 of them (N H = 384, BF16 states, one token:
     // 6.0 us, 8.3 with 16 rows), fewer rows below (N H = 6: 2.7 us with 16, 3.8 with 64); FP32
-    // states of one token stream best in the smallest pieces (N H = 3072: 71 us, 77 with 64)
+    // states of one token stream best in the smallest pieces (24 heads of 128 sequences: 71 us, 77 with 64)
     const int least = a->K == 128 ? 16 : 32;
     int rows = a->T == 1 && a->state_dtype == KDA_FP32 ? least : 64;
     while (rows > least && a->N * a->H * (a->V / rows) < 512) rows /= 2;
