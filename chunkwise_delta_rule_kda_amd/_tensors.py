@@ -53,6 +53,12 @@ def on_device(first, names, *rest):
     return first.device
 
 
+def contiguous_like(t):
+    """A contiguous uninitialised tensor of t's shape, dtype and device (of a contiguous t
+    empty_like is the shortest way there; of another it would keep the strides)."""
+    return _torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 @contextlib.contextmanager
 def _on(device, stream):
     torch = _torch

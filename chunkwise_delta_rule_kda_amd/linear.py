@@ -3,7 +3,7 @@
 import ctypes
 
 from . import KdaError, _raise_if, kda_last_error, load_library
-from ._tensors import dtype_code, get_torch, is_tensor, need, on_device, run_on
+from ._tensors import contiguous_like, dtype_code, get_torch, is_tensor, need, on_device, run_on
 
 __all__ = ["kda_linear", "kda_linear_args", "kda_linear_check", "kda_linear_plan",
            "kda_linear_workspace_bytes", "make_linear_args"]
@@ -201,9 +201,10 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
     lib = load_library()
     with run_on(dev, stream) as handle:
         if o is None:
-            o = v.new_empty(v.shape)
+            o = contiguous_like(v)
         if state_out is None and output_final_state:
-            state_out = v.new_empty((N, H, V, K), dtype=state_dtype)
+            state_out = (torch.empty_like(state_in) if state_in is not None
+                         else v.new_empty((N, H, V, K), dtype=state_dtype))
         a = kda_linear_args(
             q.data_ptr(), k.data_ptr(), v.data_ptr(), _ptr(g), _ptr(log_decay), _ptr(state_in),
             _ptr(cu_seqlens), o.data_ptr(), _ptr(state_out), None, 0, B, T, H, Hk, K, V, N,

@@ -4,7 +4,7 @@ kda_gated_norm (include/kda.h)."""
 import ctypes
 
 from . import KdaError, kda_last_error, load_library
-from ._tensors import dtype_code, get_torch, is_tensor, need, on_device, run_on
+from ._tensors import contiguous_like, dtype_code, get_torch, is_tensor, need, on_device, run_on
 
 __all__ = ["kda_gated_norm", "kda_gated_norm_args"]
 
@@ -94,9 +94,9 @@ def kda_gated_norm(x, gate=None, weight=None, residual=None, *, next_weight=None
     ptr = lambda t: None if t is None else t.data_ptr()
     with run_on(dev, stream) as handle:
         if out is None:
-            out = x.new_empty(shape)
+            out = contiguous_like(x)
         if both and next_out is None:
-            next_out = x.new_empty(shape)
+            next_out = contiguous_like(x)
         a = kda_gated_norm_args(ptr(x), ptr(gate), ptr(residual), ptr(weight), ptr(next_weight),
                                 ptr(out), ptr(next_out), M, G, D, *st, code, _ACT[gate_act], eps,
                                 scale)

@@ -116,7 +116,7 @@ def kda_pool_compact(pool, slots, *, new_slots=None, count=None, workspace=None,
         if new_slots is None:
             new_slots = torch.empty_like(slots)
         if count is None:
-            count = torch.empty(1, dtype=torch.int32, device=dev)
+            count = slots.new_empty(1)
         a = kda_pool_compact_args(p, slots.data_ptr(), new_slots.data_ptr(), count.data_ptr(), n,
                                   None, 0)
         if workspace is None:
@@ -124,7 +124,7 @@ def kda_pool_compact(pool, slots, *, new_slots=None, count=None, workspace=None,
             status = lib.kda_pool_compact_workspace_bytes(ctypes.byref(a), ctypes.byref(size))
             if status:
                 raise KdaError(status, kda_last_error())
-            workspace = torch.empty(size.value, dtype=torch.uint8, device=dev)
+            workspace = slots.new_empty(size.value // 4)  # a multiple of 256 bytes
         a.workspace = workspace.data_ptr()
         a.workspace_bytes = workspace.numel() * workspace.element_size()
         status = lib.kda_pool_compact(ctypes.byref(a), handle)
