@@ -26,8 +26,8 @@ _ACT = {"sigmoid": 0, "silu": 1}
 def _rows(t, name):
     """Strides of the rows of t seen as [M, G, D] with G its last axis but one."""
     shape, stride = t.shape, t.stride()
-    if t.is_contiguous():
-        return (stride[-3], stride[-2]) if len(shape) > 2 else (shape[-1], 0)
+    if t.is_contiguous():  # from the shape: the strides of axes of one entry say nothing
+        return (shape[-2] * shape[-1], shape[-1]) if len(shape) > 2 else (shape[-1], 0)
     if not (shape[-1] == 1 or stride[-1] == 1):
         raise KdaError(2, f"the last axis of {name} must be contiguous")
     g = stride[-2] if len(shape) > 2 and shape[-2] > 1 else 0

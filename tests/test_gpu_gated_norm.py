@@ -185,3 +185,34 @@ def test_graph_and_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("layout", ["sequence first", "heads and tokens exchanged"])
+def test_single_tokens_in_other_axis_orders(dt, layout):
+    """[B, 1, G, D] tensors that are contiguous although the strides of their token axis are
+    not those of a dense tensor, as x, gate and residual, alone and together."""
+    def make(seed):
+        if layout == "sequence first":
+            return rand(1, 5, 4, 128, dt=dt, seed=seed).transpose(0, 1)
+        return rand(5, 4, 1, 128, dt=dt, seed=seed).transpose(1, 2)
+
+    x, gate, res = make(1), make(2), make(3)
+    assert x.shape == (5, 1, 4, 128) and x.is_contiguous()
+    dense = [t.clone().as_strided(t.shape, (512, 512, 128, 1)) for t in (x, gate, res)]
+    w = 1 + 0.1 * rand(128, dt="fp32", seed=4)
+    for use in range(1, 8):
+        t = [(a if use >> i & 1 else b) for i, (a, b) in enumerate(zip((x, gate, res), dense))]
+        check(t[0], t[1], w, t[2], name=f"{layout} {use}")
+
+
+def test_one_token_of_the_linear_attention():
+    """o of kda_linear for single tokens in a sequence-first layout, normed and gated."""
+    import torch
+
+    import chunkwise_delta_rule_kda_amd as kda
+
+    q, k, v = (rand(1, 5, 4, 128, dt="bf16", seed=s).transpose(0, 1) for s in (1, 2, 3))
+    o, _ = kda.kda_linear(q, k, v)
+    assert o.shape == (5, 1, 4, 128)
+    check(o, rand(5, 1, 4, 128, dt="bf16", seed=4), name="o of kda_linear")
