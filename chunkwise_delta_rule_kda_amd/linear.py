@@ -169,6 +169,8 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
         if st[3] != 1 or st[2] != K or (H > 1 and st[1] != V * K):
             raise KdaError(2, "each state pool slot must be contiguous")
         pitch = st[0] if slots > 1 else H * V * K
+        if pitch < H * V * K:  # 0 would be taken for dense slots
+            raise KdaError(10, f"the state pool's slot pitch {pitch} is less than a slot")
         if pitch % 8:
             raise KdaError(2, "the state pool's slot pitch must be a multiple of 8 elements")
         if (state_out is not None and state_out is not state_in

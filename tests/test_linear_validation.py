@@ -304,3 +304,19 @@ def test_norm_binding():
     go(2, "last axis", x, torch.zeros(3, 4, 256)[..., ::2])
     go(2, "cannot be seen as one", torch.zeros(3, 2, 4, 128),
        torch.zeros(3, 5, 4, 128)[:, :2])
+
+
+def test_linear_pool_slots_must_not_overlap():
+    """A pool whose slots lie on one another (one state expanded) or within one another."""
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    q, v = z(2, 20, 2, 64), z(2, 20, 4, 128)
+    ids = torch.zeros(2, dtype=torch.int32)
+    go = lambda code, text, pool: expect(code, text, kda.kda_linear, q, q, v, None, pool,
+                                         ssm_state_indices=ids)
+    one = z(1, 4, 128, 64)
+    go(10, "slot pitch", one.expand(5, 4, 128, 64))
+    go(10, "slot pitch", z(9, 4, 128, 64).as_strided((5, 4, 128, 64), (128 * 64, 128 * 64, 64, 1)))
+    # one slot: its stride says nothing
+    go(2, "CUDA tensor", one.expand(1, 4, 128, 64))
+    go(2, "CUDA tensor", one.as_strided((1, 4, 128, 64), (0, 128 * 64, 64, 1)))
+    go(2, "CUDA tensor", z(5, 5, 128, 64)[:, :4])  # padded
