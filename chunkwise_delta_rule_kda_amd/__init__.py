@@ -350,8 +350,11 @@ def _validate(q, k, v, g, beta, state_in, cu_seqlens, A_log, dt_bias, lower_boun
                  "a state pool needs state_in [N_pool, H, 128, 128]")
             need(state_in.shape[0] >= 1 and state_in[0].is_contiguous(), 2,
                  "each state pool slot must be contiguous")
-            need(state_in.stride(0) % 8 == 0, 2, "the state pool's slot pitch must be a "
-                 "multiple of 8 elements")
+            # a slot pitch of 0 would be taken for dense slots
+            need(state_in.shape[0] == 1 or state_in.stride(0) >= H * D * D, 10,
+                 f"the state pool's slot pitch {state_in.stride(0)} is less than a slot")
+            need(state_in.shape[0] == 1 or state_in.stride(0) % 8 == 0, 2, "the state pool's "
+                 "slot pitch must be a multiple of 8 elements")
     elif ssm_state_indices is not None:
         raise KdaError(10, "a state pool needs state_in")
     if o is not None:
@@ -449,7 +452,8 @@ def kda_prefill(q, k, v, g, beta, state_in=None, cu_seqlens=None, *, scale=None,
         o = torch.empty_like(v)
     pool_slots = pool_pitch = 0
     if ssm_state_indices is not None:
-        pool_slots, pool_pitch = state_in.shape[0], state_in.stride(0)
+        pool_slots = state_in.shape[0]
+        pool_pitch = state_in.stride(0) if pool_slots > 1 else 0
         state_out = state_in
     if state_out is None and output_final_state:
         state_out = torch.empty((N, H, D, D), dtype=state_dtype, device=q.device)

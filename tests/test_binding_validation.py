@@ -107,3 +107,17 @@ def test_checkpoint_buffers():
     expect(2, "checkpoint_cu_starts", checkpoint_every=16,
            checkpoint_cu_starts=torch.zeros(B + 2, dtype=torch.int64))
     expect(10, "multiple of 16", checkpoint_every=24)
+
+
+def test_pool_slots_must_not_overlap():
+    """A pool expanded from one state (slot stride 0, which the C side would read as dense
+    slots) or with slots within one another; the stride of a single slot says nothing."""
+    ids = torch.zeros(B, dtype=torch.int32)
+    one = torch.zeros(1, H, D, D, dtype=torch.bfloat16)
+    expect(10, "slot pitch", state_in=one.expand(5, H, D, D), ssm_state_indices=ids)
+    long = torch.zeros(6, H, D, D, dtype=torch.bfloat16)
+    expect(10, "slot pitch", state_in=long.as_strided((5, H, D, D), (D * D, D * D, D, 1)),
+           ssm_state_indices=ids)
+    for st in (one.expand(1, H, D, D), one.as_strided((1, H, D, D), (8, D * D, D, 1)),
+               torch.zeros(5, H + 1, D, D, dtype=torch.bfloat16)[:, :H]):
+        expect(2, "must be a CUDA tensor", state_in=st, ssm_state_indices=ids)
