@@ -482,7 +482,7 @@ kda_status kda_linear_plan(const kda_linear_args* a, kda_linear_plan_info* out) 
   out->segment_tokens = pl.seg;
   out->segments_bound = pl.seg ? pl.slots : 0;
   out->workgroups = pl.slots * a->H * (a->V / pl.rows);
-  out->state_workgroups = pl.seg ? out->workgroups : 0;
+  out->state_workgroups = pl.seg ? pl.slots * a->H * (a->V / kda::kLinRows) : 0;
   out->workspace_bytes = pl.bytes;
   return KDA_OK;
 }

@@ -320,3 +320,18 @@ def test_linear_pool_slots_must_not_overlap():
     go(2, "CUDA tensor", one.expand(1, 4, 128, 64))
     go(2, "CUDA tensor", one.as_strided((1, 4, 128, 64), (0, 128 * 64, 64, 1)))
     go(2, "CUDA tensor", z(5, 5, 128, 64)[:, :4])  # padded
+
+
+def test_linear_plan_of_128_row_workgroups():
+    """The segments' state launch has 64 value rows per workgroup whatever the outputs have."""
+    for kw in (dict(H=200, T=256, segment_tokens=64), dict(H=200, T=1000, V=256, segment_tokens=128),
+               dict(H=40, T=8192)):
+        p = kda.kda_linear_plan(lin(**kw))
+        assert p["value_block"] == 128 and p["segment_tokens"] > 0, (kw, p)
+        heads = kw["H"] * p["segments_bound"]
+        assert p["workgroups"] == heads * kw.get("V", 128) // 128
+        assert p["state_workgroups"] == heads * kw.get("V", 128) // 64
+    p = kda.kda_linear_plan(lin(H=6, T=8192))
+    assert p["value_block"] == 64 and p["state_workgroups"] == p["workgroups"] > 0
+    p = kda.kda_linear_plan(lin(H=200, T=256, segment_tokens=-1))
+    assert p["value_block"] == 128 and p["state_workgroups"] == 0
