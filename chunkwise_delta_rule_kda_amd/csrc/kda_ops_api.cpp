@@ -215,10 +215,12 @@ kda_status linear_sizes(const kda_linear_args* a, LinPlan* out) {
   if ((tokens / kda::kLinChunk + a->N) * a->H * a->V * a->K > (Wide(1) << 56))
     return fail(KDA_ERR_SHAPE, "too many chunks");
   const LinPlan pl = linear_plan(a);
-  // the token loop's launch, or the scan's and the chunks'
+  // the token loop's launch, or the scan's and the larger one of the states' (always by
+  // kLinRows) and the outputs'
   const Wide pairs = static_cast<Wide>(a->N) * a->H;
   const Wide threads = pl.tokens ? pairs * (a->V / pl.rows) * 256
-                                 : (static_cast<Wide>(pl.slots) * a->H + 8) * (a->V / pl.rows) * 512;
+                                 : (static_cast<Wide>(pl.slots) * a->H + 8) *
+                                       (a->V / (pl.seg ? kda::kLinRows : pl.rows)) * 512;
   if (threads > kMaxThreads || (pl.seg && pairs * ceil_div(a->V * a->K, 1024) * 256 > kMaxThreads))
     return fail(KDA_ERR_SHAPE, "too much for one launch (N*H, or segments*H)");
   *out = pl;

@@ -335,3 +335,18 @@ def test_linear_plan_of_128_row_workgroups():
     assert p["value_block"] == 64 and p["state_workgroups"] == p["workgroups"] > 0
     p = kda.kda_linear_plan(lin(H=200, T=256, segment_tokens=-1))
     assert p["value_block"] == 128 and p["state_workgroups"] == 0
+
+
+def test_segments_past_one_state_launch_are_refused():
+    """128-row workgroups for the outputs, twice as many of 64 rows for the segments' states:
+    the larger launch has to stay below 2^32 threads, 2^22 (segment, head) pairs of V = 128."""
+    far = dict(H=256, V=128, g=None, log_decay=None, state_in=None, state_out=None, q=at(0), k=at(500),
+               v=at(1000), o=at(1500), workspace=at(2000), workspace_bytes=1 << 40, segment_tokens=64)
+    most = (1 << 14) - 1  # segments of 256 heads, with the launch's rounding up
+    p = kda.kda_linear_plan(lin(T=64 * most, **far))
+    assert p["value_block"] == 128 and p["segment_tokens"] == 64
+    assert p["state_workgroups"] * 512 < 1 << 32
+    assert status(T=64 * most, **far) == 0, kda.kda_last_error()
+    for T in (64 * (most + 1), 64 * 20000, 64 * 32000):
+        assert status(T=T, **far) == 2, T
+        assert "one launch" in kda.kda_last_error()
