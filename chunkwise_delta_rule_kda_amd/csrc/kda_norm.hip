@@ -153,29 +153,40 @@ __global__ __launch_bounds__(THREADS) void norm_wide_kernel(NormParams p) {
   });
 }
 
-template <bool BF16>
-hipError_t go(const NormParams& p, hipStream_t stream) {
-  const int64_t rows = p.M * p.G;
-  auto narrow = [&](auto kernel, int lanes) {
-    const int64_t per = 256 / lanes;
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>((rows + per - 1) / per)), dim3(256), 0, stream, p);
-  };
-  auto wide = [&](auto kernel, int threads) {
-    hipLaunchKernelGGL(kernel, dim3(static_cast<unsigned>(rows)), dim3(threads), 0, stream, p);
-  };
-  if (p.D <= 64) narrow(norm_narrow_kernel<BF16, 8>, 8);
-  else if (p.D <= 128) narrow(norm_narrow_kernel<BF16, 16>, 16);
-  else if (p.D <= 256) narrow(norm_narrow_kernel<BF16, 32>, 32);
-  else if (p.D <= 512) narrow(norm_narrow_kernel<BF16, 64>, 64);
-  else if (p.D <= 1024) wide(norm_wide_kernel<BF16, 128, 1>, 128);
-  else if (p.D <= 2048) wide(norm_wide_kernel<BF16, 256, 1>, 256);
-  else if (p.D <= 4096) wide(norm_wide_kernel<BF16, 256, 2>, 256);
-  else if (p.D <= 6144) wide(norm_wide_kernel<BF16, 256, 3>, 256);
-  else if (p.D <= 8192) wide(norm_wide_kernel<BF16, 512, 2>, 512);
-  else if (p.D <= 12288) wide(norm_wide_kernel<BF16, 512, 3>, 512);
-  else wide(norm_wide_kernel<BF16, 512, 4>, 512);
+template <bool BF16, int LANES>
+hipError_t narrow(const NormParams& p, hipStream_t stream) {
+  const int64_t rows = p.M * p.G, per = 256 / LANES;
+  hipLaunchKernelGGL((norm_narrow_kernel<BF16, LANES>), dim3(static_cast<unsigned>((rows + per - 1) / per)),
+                     dim3(256), 0, stream, p);
   return hipGetLastError();
 }
+
+template <bool BF16, int THREADS, int NV>
+hipError_t wide(const NormParams& p, hipStream_t stream) {
+  hipLaunchKernelGGL((norm_wide_kernel<BF16, THREADS, NV>), dim3(static_cast<unsigned>(p.M * p.G)),
+                     dim3(THREADS), 0, stream, p);
+  return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t go(const NormParams& p, hipStream_t stream) {
+  const int threads = norm_threads(p.D);
+  const int pieces = (p.D / 8 + threads - 1) / threads;  // of eight elements, per thread
+  switch (threads) {
+    case 8: return narrow<BF16, 8>(p, stream);
+    case 16: return narrow<BF16, 16>(p, stream);
+    case 32: return narrow<BF16, 32>(p, stream);
+    case 64: return narrow<BF16, 64>(p, stream);
+    case 128: return wide<BF16, 128, 1>(p, stream);
+    case 256:
+      return pieces == 1 ? wide<BF16, 256, 1>(p, stream)
+             : pieces == 2 ? wide<BF16, 256, 2>(p, stream) : wide<BF16, 256, 3>(p, stream);
+    default:
+      return pieces == 2 ? wide<BF16, 512, 2>(p, stream)
+             : pieces == 3 ? wide<BF16, 512, 3>(p, stream) : wide<BF16, 512, 4>(p, stream);
+  }
+}
+static_assert(kNormMax == 8 * 512 * 4, "the widest row is four pieces of 512 threads");
 
 }  // namespace
 

@@ -324,10 +324,8 @@ bool same_pool(const kda_pool* a, const kda_pool* b) {
          a->slot_pitch == b->slot_pitch && (a->layers == 1 || a->layer_pitch == b->layer_pitch);
 }
 
-constexpr int64_t kCopyGroup = 8192;  // elements of a slot per workgroup
-
 kda_status grid_of(const kda_pool* p, int64_t pairs) {
-  if (static_cast<Wide>(ceil_div(p->slot_elems, kCopyGroup)) * p->layers * pairs * 256 > kMaxThreads)
+  if (static_cast<Wide>(ceil_div(p->slot_elems, kda::kCopyGroup)) * p->layers * pairs * 256 > kMaxThreads)
     return fail(KDA_ERR_SHAPE, "pairs x layers x slot_elems are too many for one launch");
   return KDA_OK;
 }
@@ -397,19 +395,13 @@ kda_status compact_check(const kda_pool_compact_args* a) {
 
 // ------------------------------------------------------------ gated norm
 
-// Threads of a row's workgroup or part of a wave (kda_norm.hip).
-int64_t norm_threads(int64_t D) {
-  int64_t t = 8;
-  while (t < 256 && 8 * t < D) t *= 2;
-  return D <= 6144 ? t : 512;
-}
-
 kda_status norm_check(const kda_gated_norm_args* a) {
   if (!a) return fail(KDA_ERR_NULL, "args is NULL");
-  if (a->D < 8 || a->D > 16384 || a->D % 8)
-    return fail(KDA_ERR_SHAPE, "D=%lld is not a multiple of 8 up to 16384", (long long)a->D);
+  if (a->D < 8 || a->D > kda::kNormMax || a->D % 8)
+    return fail(KDA_ERR_SHAPE, "D=%lld is not a multiple of 8 up to %d", (long long)a->D,
+                kda::kNormMax);
   if (a->M < 0 || a->M > kBig || a->G < 1 || a->G > kBig ||
-      static_cast<Wide>(a->M) * a->G * norm_threads(a->D) > kMaxThreads - 256)
+      static_cast<Wide>(a->M) * a->G * kda::norm_threads(a->D) > kMaxThreads - 256)
     return fail(KDA_ERR_SHAPE, "M=%lld G=%lld D=%lld", (long long)a->M, (long long)a->G, (long long)a->D);
   if (!known_dtype(a->io_dtype)) return fail(KDA_ERR_DTYPE, "io_dtype %d", a->io_dtype);
   if (a->act != KDA_ACT_SIGMOID && a->act != KDA_ACT_SILU)

@@ -60,6 +60,9 @@ hipError_t launch_linear_scan(const LinParams& p, int k_dim, hipStream_t stream)
 hipError_t launch_linear_tokens(const LinParams& p, int k_dim, bool io_bf16, int rows,
                                 hipStream_t stream);
 
+constexpr int kCopyUnits = 4;                          // pieces of eight elements per thread
+constexpr int kCopyGroup = 256 * kCopyUnits * 8;       // elements of a slot per workgroup
+
 struct PoolCopy {
   const void* src;
   void* dst;
@@ -76,6 +79,16 @@ hipError_t launch_pool_copy(const PoolCopy& p, hipStream_t stream);
 hipError_t launch_pool_plan(const int32_t* idx, int32_t* new_idx, int32_t* count, int64_t n,
                             int64_t slots, int32_t* move_src, int32_t* move_dst,
                             int32_t* moves, hipStream_t stream);
+
+constexpr int kNormMax = 16384;  // longest row
+
+// Threads of a row of D elements: part of a wave up to D = 512, a workgroup beyond.
+inline int norm_threads(int64_t D) {
+  if (D > 6144) return 512;
+  int t = 8;
+  while (t < 256 && 8 * t < D) t *= 2;
+  return t;
+}
 
 struct NormParams {
   const void* x;

@@ -8,14 +8,11 @@ namespace kda {
 
 namespace {
 
-// A workgroup copies 256 x kUnits x 8 consecutive elements of one slot of one layer, all
+// A workgroup copies kCopyGroup consecutive elements of one slot of one layer, all
 // loads before the first store. Bound by its bytes: 48 slots of 24 heads in four layers from
 // FP32 to BF16, 434 MB, 90 us (4.8 TB/s); 120 slots x 24 heads x two layers of FP32,
 // 755 MB, 146 us (5.2 TB/s). Pairs are known on the device only, so a compaction launches a
 // grid for the most moves there can be; a workgroup without one ends at once.
-constexpr int kUnits = 4;
-constexpr int kPerGroup = 256 * kUnits * 8;
-
 template <bool SRC_BF16, bool DST_BF16>
 __global__ __launch_bounds__(256) void pool_copy_kernel(PoolCopy p, int64_t blocks) {
   const int64_t b = blockIdx.x;
@@ -26,14 +23,14 @@ __global__ __launch_bounds__(256) void pool_copy_kernel(PoolCopy p, int64_t bloc
   const int64_t si = p.src_idx[pair], di = p.dst_idx[pair];
   if (di < 0 || di >= p.dst_slots) return;
   const bool held = si >= 0 && si < p.src_slots;
-  const int64_t first = (b - row * blocks) * kPerGroup + 8 * threadIdx.x;
+  const int64_t first = (b - row * blocks) * kCopyGroup + 8 * threadIdx.x;
   constexpr int kSrc = SRC_BF16 ? 2 : 4, kDst = DST_BF16 ? 2 : 4;
   const char* from = static_cast<const char*>(p.src) + (si * p.src_pitch + layer * p.src_layer) * kSrc;
   char* to = static_cast<char*>(p.dst) + (di * p.dst_pitch + layer * p.dst_layer) * kDst;
   if (SRC_BF16 == DST_BF16 && held && from == to) return;  // a slot onto itself
-  u32x4 x[kUnits][SRC_BF16 ? 1 : 2];
+  u32x4 x[kCopyUnits][SRC_BF16 ? 1 : 2];
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < kCopyUnits; ++u) {
     const int64_t e = first + u * 2048;
 #pragma unroll
     for (int w = 0; w < (SRC_BF16 ? 1 : 2); ++w) {
@@ -42,7 +39,7 @@ __global__ __launch_bounds__(256) void pool_copy_kernel(PoolCopy p, int64_t bloc
     }
   }
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) {
+  for (int u = 0; u < kCopyUnits; ++u) {
     const int64_t e = first + u * 2048;
     if (e >= p.slot_elems) continue;
     u32x4* w = reinterpret_cast<u32x4*>(to + e * kDst);
@@ -126,7 +123,7 @@ __global__ __launch_bounds__(1024) void pool_plan_kernel(const int32_t* idx, int
 }  // namespace
 
 hipError_t launch_pool_copy(const PoolCopy& p, hipStream_t stream) {
-  const int64_t blocks = (p.slot_elems + kPerGroup - 1) / kPerGroup;
+  const int64_t blocks = (p.slot_elems + kCopyGroup - 1) / kCopyGroup;
   const int64_t wgs = blocks * p.layers * p.pairs;
   if (wgs <= 0) return hipSuccess;
   const dim3 grid(static_cast<unsigned>(wgs));
