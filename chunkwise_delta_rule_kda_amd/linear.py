@@ -152,6 +152,8 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
         is_tensor(log_decay, "log_decay", torch.float32)
         if not (log_decay.shape == (H,) and log_decay.is_contiguous()):
             raise KdaError(2, f"log_decay must be a contiguous [{H}]")
+    if state_in is not None:
+        is_tensor(state_in, "state_in")
     if state_dtype is None:
         state_dtype = state_in.dtype if state_in is not None else dt
     st_code = 0 if state_dtype == torch.bfloat16 else 1
@@ -160,7 +162,6 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
     slots = pitch = 0
     if ssm_state_indices is not None:
         need(state_in is not None, 10, "a state pool needs state_in")
-        is_tensor(state_in, "state_in")
         need(state_in.dim() == 4 and state_in.shape[0] >= 1, 2,
              "a state pool needs state_in [slots, H, V, K]")
         slots = state_in.shape[0]
@@ -173,9 +174,10 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
             raise KdaError(10, f"the state pool's slot pitch {pitch} is less than a slot")
         if pitch % 8:
             raise KdaError(2, "the state pool's slot pitch must be a multiple of 8 elements")
-        if (state_out is not None and state_out is not state_in
-                and state_out.data_ptr() != state_in.data_ptr()):
-            raise KdaError(6, "with a state pool, state_out must be None or state_in")
+        if state_out is not None and state_out is not state_in:
+            is_tensor(state_out, "state_out")
+            if state_out.data_ptr() != state_in.data_ptr():
+                raise KdaError(6, "with a state pool, state_out must be None or state_in")
         state_out = state_in
         for name, ids in (("ssm_state_indices", ssm_state_indices),
                           ("state_out_indices", state_out_indices)):
@@ -196,6 +198,7 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
         if not (o.shape == v.shape and o.dtype == dt and o.is_contiguous()):
             raise KdaError(2, f"o must be a contiguous {tuple(v.shape)} of {dt}")
     if workspace is not None:
+        is_tensor(workspace, "workspace")
         need(workspace.is_contiguous(), 2, "workspace must be contiguous")
     dev = on_device(q, "q k v g log_decay state_in cu_seqlens o state_out workspace "
                     "ssm_state_indices state_out_indices", k, v, g, log_decay, state_in, cu_seqlens,

@@ -108,6 +108,7 @@ def kda_pool_compact(pool, slots, *, new_slots=None, count=None, workspace=None,
         _index(count, "count")
         need(count.numel() == 1, 2, "count must have one entry")
     if workspace is not None:
+        is_tensor(workspace, "workspace")
         need(workspace.is_contiguous(), 2, "workspace must be contiguous")
     dev = on_device(pool, "pool slots new_slots count workspace", slots, new_slots, count,
                     workspace)

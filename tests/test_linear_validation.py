@@ -350,3 +350,26 @@ def test_segments_past_one_state_launch_are_refused():
     for T in (64 * (most + 1), 64 * 20000, 64 * 32000):
         assert status(T=T, **far) == 2, T
         assert "one launch" in kda.kda_last_error()
+
+
+def test_arguments_that_are_no_tensors_are_refused():
+    """With a KdaError, as every other argument that is not what it should be."""
+    z = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)
+    q, v, pool = z(2, 20, 2, 64), z(2, 20, 4, 128), z(5, 4, 128, 64)
+    ids = torch.zeros(2, dtype=torch.int32)
+    for bad in (3, [1.0], "state"):
+        for kw in (dict(state_in=bad), dict(state_in=bad, ssm_state_indices=ids),
+                   dict(state_out=bad), dict(state_in=pool, ssm_state_indices=ids, state_out=bad),
+                   dict(workspace=bad), dict(g=bad), dict(log_decay=bad), dict(cu_seqlens=bad),
+                   dict(o=bad), dict(state_in=pool, ssm_state_indices=bad),
+                   dict(state_in=pool, ssm_state_indices=ids, state_out_indices=bad)):
+            expect(2, "must be a tensor", kda.kda_linear, q, q, v, **kw)
+        for kw in (dict(pool=bad), dict(slots=bad), dict(new_slots=bad), dict(count=bad),
+                   dict(workspace=bad)):
+            expect(2, "must be a tensor", kda.kda_pool_compact,
+                   **{**dict(pool=torch.zeros(5, 64), slots=ids), **kw})
+        for kw in (dict(pool=bad), dict(src=bad), dict(dst=bad), dict(source=bad)):
+            expect(2, "must be a tensor", kda.kda_pool_copy,
+                   **{**dict(pool=torch.zeros(5, 64), src=ids, dst=ids), **kw})
+        for name in ("x", "gate", "weight", "residual", "next_weight", "out", "next_out"):
+            expect(2, "must be a tensor", kda.kda_gated_norm, **{"x": torch.zeros(2, 64), name: bad})
