@@ -118,7 +118,7 @@ __device__ __forceinline__ void by_wave(int wave, F f) {
 // registers, write them to LDS, and form the scores beside the other four's products with
 // the state; those add P V while the next tiles are written. Two tiles of each kind do not
 // fit the LDS (a stage is 80 KB). 2 x 1999 tokens x 12 heads (240 workgroups of at most seven
-// chunks): 60 us, the matrix pipes busy 65 % of it; operands read one group ahead of their
+// chunks): 59 us, the matrix pipes busy 65 % of it; operands read one group ahead of their
 // products spilled (86 us).
 template <int KD>
 __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) void linear_f32_kernel(LinParams p) {
@@ -249,13 +249,15 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 //   scores of chunk c and the decay factors of chunk c + 1.
 // * Four state waves add P V of chunk c - 1 to its outputs and store them, form the
 //   outputs of chunk c from the entering state, and update the state.
-// The LDS bounds it: 362 LDS instructions per chunk of 64 rows (each state wave reads all of
-// Q and K), at best 6 to 7.2 clocks each in a compute unit, of the 3000 clocks (1.33 us) that
-// a chunk takes; the matrix pipes are busy for 770 of them, the vector units for 1430.
-// 128 rows per workgroup read Q and K once for twice the rows, 4400 clocks a chunk, but are
-// half as many workgroups: the geometry's model chooses (kda_ops_api.cpp). 8192 tokens x 96
-// heads: 247 us (815 MB, 3.3 TB/s); four waves with two barriers per chunk and tiles through
-// registers took 377.
+// The chain through a chunk bounds it, no unit alone: of the 3000 clocks (1.33 us) that a chunk
+// of 64 rows takes within the last-level cache the LDS is active for 1405 (362 instructions,
+// each state wave reads all of Q and K), the vector units for 1430, the matrix pipes for 770.
+// With one wave of each kind per SIMD there is little to fill the gaps: over 8192 tokens x 96
+// heads (3920 clocks a chunk, from memory) the waves wait for data or the barrier 30 % of
+// their time and to be issued 39 %. 128 rows per workgroup read Q and K once for twice the
+// rows, 4400 clocks a chunk, but are half as many workgroups: the geometry's model chooses
+// (kda_ops_api.cpp). 8192 tokens x 96 heads: 247 us (815 MB, 3.3 TB/s); four waves with two
+// barriers per chunk and tiles through registers took 377.
 constexpr int kStages = 3;
 
 template <int KD, int NC, int PARTS>

@@ -11,9 +11,9 @@ namespace {
 // (kda_linear_chunks.hip): four load the tiles of chunk c + 2 into a ring of three and make
 // the decay factors of chunk c + 1, four update the state. Z_p goes to the segment's scan
 // slot, the segment's total decay to scan_d. A segment is a chain of chunks, so the launch
-// is as long as one: 8192 tokens x 6 heads in 19 segments of seven chunks 12.4 us (1.5 us a
+// is as long as one: 8192 tokens x 6 heads in 19 segments of seven chunks 12.5 us (1.5 us a
 // chunk and the launch); FP32 I/O, bound by its matrix products, 2 x 1999 tokens x 12 heads
-// 25.7 us (28.8 by four waves that also loaded the tiles).
+// 25.2 us (28.8 by four waves that also loaded the tiles).
 constexpr int kStages = 3;
 
 template <bool BF16, int KD, int PARTS>
@@ -142,7 +142,7 @@ __global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2, 4))) voi
 }
 
 // S_{p+1} = D_p S_p + Z_p over the segments of one (sequence, head), elementwise and bound
-// by the latency of its loads (19 segments x 6 heads, 15 MB: 5.4 us): a
+// by the latency of its loads (19 segments x 6 heads, 15 MB: 5.5 us): a
 // thread carries four elements of the state and leaves every segment's start state in its
 // slot. The first segment's slot gets the sequence's initial state, so that the launch
 // that follows reads no state another workgroup of it writes (in-place updates).

@@ -3,9 +3,9 @@
 //   S <- exp(g) S + v k^T ; o = s S q
 // Each state is read once, takes the T steps in FP32 registers and is written once, so
 // the launch is bound by the state traffic: 128 sequences x 24 heads of FP32 states, 404 MB
-// in 77 us (5.2 TB/s, the rate of a large copy). A row of the state is K / 8 lanes of eight
+// in 73 us (5.5 TB/s, as a copy of 256 MB), 78 between scattered slots of a pool. A row of the state is K / 8 lanes of eight
 // keys each; rows never meet, so a (sequence, head) is split over workgroups of `rows`
-// value rows where there are few of them (one sequence of 6 heads: 2.7 us by 16 rows, 3.8
+// value rows where there are few of them (one sequence of 6 heads: 3.4 us by 16 rows, 4.3
 // by 64).
 
 #include "kda_device.h"

@@ -3,7 +3,7 @@
 //   z = next_weight * y / sqrt(mean(y^2) + eps)
 // A row is held in registers between its two reductions, so every tensor is read or
 // written once; the launch is bound by those bytes: 8192 x 12288 BF16 with gate, residual
-// and the next norm, 1007 MB in 182 us (5.5 TB/s); 8192 x 96 heads of 128 with a gate
+// and the next norm, 1007 MB in 182 to 190 us by the run (5.3 to 5.5 TB/s); 8192 x 96 heads of 128 with a gate
 // 111 us (5.4 TB/s). Rows of at most 512 elements share a wave; wider ones are a workgroup
 // of as many threads as keep at most three or four pieces of eight each (2048 x 16384: 37 us
 // by 512 threads, 50 by 256 with twice the registers).

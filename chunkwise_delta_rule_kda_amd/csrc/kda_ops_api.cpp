@@ -122,8 +122,9 @@ LinPlan linear_plan(const kda_linear_args* a) {
   if (linear_token_form(a)) {
     pl.tokens = true;
     // 64 rows per workgroup where that gives 512 of them (N H = 384, BF16 states, one token:
-    // 6.0 us, 8.3 with 16 rows), fewer rows below (N H = 6: 2.7 us with 16, 3.8 with 64); FP32
-    // states of one token stream best in the smallest pieces (24 heads of 128 sequences: 71 us, 77 with 64)
+    // 6.9 us, 9.3 with 16 rows; 24 heads of 128: 34 and 46), fewer rows below (N H = 6: 3.4 us with
+    // 16, 4.3 with 64); FP32 states of one token stream best in the smallest pieces (24 heads of
+    // 128 sequences: 73.0 us with 16 rows, 74.4 with 32, 76.4 with 64; 96 of 64: 142, 147, 150)
     const int least = a->K == 128 ? 16 : 32;
     int rows = a->T == 1 && a->state_dtype == KDA_FP32 ? least : 64;
     while (rows > least && a->N * a->H * (a->V / rows) < 512) rows /= 2;
@@ -154,7 +155,11 @@ LinPlan linear_plan(const kda_linear_args* a) {
   const bool cached = bytes <= 256e6;
   // 128 rows of an FP32 state (its updates in three parts) do not fit the registers
   const int most = bf16 && a->state_dtype == KDA_BF16 && a->V % 128 == 0 ? 128 : 64;
-  // a packed batch's longest sequence is taken for 1.75 times the mean
+  // The host does not know a packed batch's lengths. Its longest sequence is taken for 1.75
+  // times the mean, not for the mean, since a wrong choice costs more where lengths are
+  // uneven: two sequences, T = 2386, H = 20, are cut and take 35 to 37 us whatever their
+  // lengths; serial 31 at 1 : 1, 38 at 2 : 1, 48 at 7 : 1 (T = 6678, H = 38: 87 to 103 cut; 75,
+  // 97 and 124 serial). One long prompt among many short ones is a longer chain than this.
   const double steps = a->cu_seqlens && a->N > 1
                            ? std::fmin(1.0, 1.75 / static_cast<double>(a->N)) * static_cast<double>(a->T) / 64
                            : static_cast<double>(a->T) / 64;

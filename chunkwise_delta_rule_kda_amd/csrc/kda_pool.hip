@@ -11,7 +11,7 @@ namespace {
 // A workgroup copies kCopyGroup consecutive elements of one slot of one layer, all
 // loads before the first store. Bound by its bytes: 48 slots of 24 heads in four layers from
 // FP32 to BF16, 434 MB, 90 us (4.8 TB/s); 120 slots x 24 heads x two layers of FP32,
-// 755 MB, 146 us (5.2 TB/s). Pairs are known on the device only, so a compaction launches a
+// 755 MB, 149 us (5.1 TB/s). Pairs are known on the device only, so a compaction launches a
 // grid for the most moves there can be; a workgroup without one ends at once.
 template <bool SRC_BF16, bool DST_BF16>
 __global__ __launch_bounds__(256) void pool_copy_kernel(PoolCopy p, int64_t blocks) {
@@ -63,7 +63,7 @@ constexpr int kWords = KDA_POOL_COMPACT_SLOTS / 32;
 // One workgroup: a bitmap of the live slots and its running counts in LDS. rank(s) is the
 // number of live slots below s; with L live ones in all, the free slot s < L is hole
 // number s - rank(s), and the live slot s >= L is move number rank(s) - rank(L). Bound by
-// the latency of its few passes: 2.6 us for 64 slots, 3.7 for 512.
+// the latency of its few passes: 2.8 us for 64 slots, 4.8 for 512.
 __global__ __launch_bounds__(1024) void pool_plan_kernel(const int32_t* idx, int32_t* new_idx,
                                                          int32_t* count, int64_t n, int slots,
                                                          int32_t* move_src, int32_t* move_dst,

@@ -91,7 +91,7 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
     last axis has to be contiguous (the other strides multiples of 8), so slices of one
     projection are taken as they are. g: [B, T, H] log decays (<= 0; -inf empties the
     state) of q's dtype or fp32, or None. log_decay: fp32 [H], a fixed decay of each head,
-    or None; where both are given they add.
+    or None; where both are given they add. scale: None (or 0) is 1 / sqrt(K).
     state_in: [N, H, V, K] or None (zeros); state_out=state_in updates in place.
     cu_seqlens: int64 [N + 1] (B = 1) or None.
     1 <= T <= 8 in the fixed layout is the step of single (or a few draft) tokens: each state

@@ -525,7 +525,8 @@ kda_status kda_pool_compact(const kda_pool_compact_args *a, void *stream);
  *     y = residual + scale * act(gate) * weight * x / sqrt(mean(x^2) + eps)
  *     z = next_weight * y / sqrt(mean(y^2) + eps)
  *
- * over rows of D elements, in FP32, each result rounded once (z from the unrounded y).
+ * over rows of D elements, in FP32, each result rounded once (z from the unrounded y). The
+ * squares are FP32 as well: entries past 1.8e19 in magnitude overflow them.
  * gate, weight and residual may be NULL (1, 1 and 0); z is written when next_out is set
  * (next_weight NULL: 1).
  */
