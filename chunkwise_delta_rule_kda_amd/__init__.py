@@ -15,6 +15,10 @@ Entry points (same names as the C ABI):
     kda_pool_copy(pool, src, dst, ...), kda_pool_compact(pool, slots, ...): slots of a
         state pool copied, forked, restored, cleared and compacted
     kda_gated_norm(x, gate, weight, residual, ...): RMS norm, gate, residual and next norm
+    kda_short_conv(x, weight, bias=None, state_in=None, cu_seqlens=None, ...) -> (out,
+        state_out): the short causal convolution in front of a recurrence
+    kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seqlens=None,
+        ...) -> (out, state_out): the recurrence with one decay per channel and state
 """
 
 import ctypes
@@ -182,13 +186,15 @@ def load_library():
     lib.kda_debug_check_cu_seqlens.argtypes = [ctypes.c_void_p, ctypes.c_int64,
                                                ctypes.c_int64, ctypes.c_void_p]
     lib.kda_debug_check_cu_seqlens.restype = ctypes.c_int
-    for name in ("kda_linear", "kda_pool_copy", "kda_pool_compact", "kda_gated_norm"):
+    for name in ("kda_linear", "kda_pool_copy", "kda_pool_compact", "kda_gated_norm",
+                 "kda_short_conv", "kda_selective_scan"):
         getattr(lib, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
         getattr(lib, name).restype = ctypes.c_int
         getattr(lib, name + "_check").argtypes = [ctypes.c_void_p]
         getattr(lib, name + "_check").restype = ctypes.c_int
     for name in ("kda_linear_workspace_bytes", "kda_linear_plan",
-                 "kda_pool_compact_workspace_bytes"):
+                 "kda_pool_compact_workspace_bytes", "kda_selective_scan_workspace_bytes",
+                 "kda_selective_scan_plan"):
         getattr(lib, name).argtypes = [ctypes.c_void_p, ctypes.c_void_p]
         getattr(lib, name).restype = ctypes.c_int
     lib.kda_abi_version.argtypes = []
@@ -516,9 +522,12 @@ def kda_prefill_no_alloc(q, k, v, g, beta, state_in=None, cu_seqlens=None, **kw)
 
 
 # The operators beside kda_prefill use the names above.
+from .conv import *  # noqa: E402,F401,F403
 from .linear import *  # noqa: E402,F401,F403
 from .norm import *  # noqa: E402,F401,F403
 from .pool import *  # noqa: E402,F401,F403
-from . import linear as _linear, norm as _norm, pool as _pool  # noqa: E402
+from .scan import *  # noqa: E402,F401,F403
+from . import conv as _conv, linear as _linear, norm as _norm  # noqa: E402
+from . import pool as _pool, scan as _scan  # noqa: E402
 
-__all__ += _linear.__all__ + _norm.__all__ + _pool.__all__
+__all__ += _linear.__all__ + _norm.__all__ + _pool.__all__ + _conv.__all__ + _scan.__all__

@@ -93,3 +93,88 @@ def run_on(device, stream):
     if stream is None and _torch.cuda.current_device() == device.index:
         return _Current(_raw_stream(device.index))
     return _on(device, stream)
+
+
+def sequences(cu_seqlens, B):
+    """The number of sequences of a call: B, or those that cu_seqlens packs into one row."""
+    if cu_seqlens is None:
+        return B
+    is_tensor(cu_seqlens, "cu_seqlens", _torch.int64)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise KdaError(2, "cu_seqlens must be a 1-D tensor of N + 1 >= 2 offsets")
+    if not cu_seqlens.is_contiguous():
+        raise KdaError(2, "cu_seqlens must be contiguous")
+    if B != 1:
+        raise KdaError(2, f"packed varlen needs B = 1 (got {B})")
+    return cu_seqlens.numel() - 1
+
+
+def channel_strides(t, name, B, T):
+    """Batch and token stride of a [B, T, channels] tensor whose channels are contiguous."""
+    s = t.stride()
+    if s[2] != 1 and t.shape[2] != 1 and B and T:
+        raise KdaError(2, f"the last axis of {name} must be contiguous")
+    # the stride of an axis of one entry says nothing
+    return (0 if B == 1 else s[0]), (0 if T == 1 else s[1])
+
+
+def _state_check(t, name, shape, dtype):
+    is_tensor(t, name)
+    if t.shape != shape:
+        raise KdaError(2, f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if t.dtype != dtype:
+        raise KdaError(3, f"{name} is {t.dtype}, the state dtype is {dtype}")
+
+
+def states(state_in, state_out, state_dtype, io_dtype, N, a, b, ssm_state_indices,
+           state_out_indices):
+    """Checks of the state arguments of an operator whose states are [N, a, b] (with
+    ssm_state_indices a pool [slots, a, b]): (state_out, dtype, its code, slots, pitch)."""
+    torch = _torch
+    if state_in is not None:
+        is_tensor(state_in, "state_in")
+    if state_dtype is None:
+        state_dtype = io_dtype if state_in is None else state_in.dtype
+    code = KDA_FP32 if state_dtype == torch.float32 else KDA_BF16
+    if code == KDA_BF16 and state_dtype != torch.bfloat16:
+        raise KdaError(3, f"state dtype {state_dtype}")
+    if ssm_state_indices is None:
+        need(state_out_indices is None, 10, "state_out_indices needs ssm_state_indices")
+        for name, t in (("state_in", state_in), ("state_out", state_out)):
+            if t is not None:
+                _state_check(t, name, (N, a, b), state_dtype)
+                if not t.is_contiguous():
+                    raise KdaError(2, f"{name} must be contiguous")
+        return state_out, state_dtype, code, 0, 0
+    need(state_in is not None, 10, "a state pool needs state_in")
+    if state_in.dim() != 3 or state_in.shape[0] < 1:
+        raise KdaError(2, f"a state pool needs state_in [slots, {a}, {b}]")
+    slots = state_in.shape[0]
+    _state_check(state_in, "the state pool", (slots, a, b), state_dtype)
+    st = state_in.stride()
+    if st[2] != 1 or (a > 1 and st[1] != b):
+        raise KdaError(2, "each state pool slot must be contiguous")
+    pitch = st[0] if slots > 1 else a * b
+    if pitch < a * b:  # 0 would be taken for dense slots
+        raise KdaError(10, f"the state pool's slot pitch {pitch} is less than a slot")
+    if pitch % 8:
+        raise KdaError(2, "the state pool's slot pitch must be a multiple of 8 elements")
+    if state_out is not None and state_out is not state_in:
+        is_tensor(state_out, "state_out")
+        if state_out.data_ptr() != state_in.data_ptr():
+            raise KdaError(6, "with a state pool, state_out must be None or state_in")
+    for name, ids in (("ssm_state_indices", ssm_state_indices),
+                      ("state_out_indices", state_out_indices)):
+        if ids is not None:
+            is_tensor(ids, name, torch.int32)
+            if ids.shape != (N,) or not ids.is_contiguous():
+                raise KdaError(2, f"{name} must be a contiguous [{N}]")
+    return state_in, state_dtype, code, slots, pitch
+
+
+def vector(t, name, n):
+    """An optional FP32 [n]."""
+    if t is not None:
+        is_tensor(t, name, _torch.float32)
+        if t.shape != (n,) or not t.is_contiguous():
+            raise KdaError(2, f"{name} must be a contiguous [{n}]")

@@ -17,9 +17,11 @@ LIB = os.path.join(PKG, "libkda.so")
 
 SOURCES = ["kda_api.cpp", "kda_prepare.hip", "kda_recurrence.hip", "kda_fused.hip",
            "kda_decode.hip", "kda_ops_api.cpp", "kda_linear_chunks.hip",
-           "kda_linear_states.hip", "kda_linear_tokens.hip", "kda_pool.hip", "kda_norm.hip"]
+           "kda_linear_states.hip", "kda_linear_tokens.hip", "kda_pool.hip", "kda_norm.hip",
+           "kda_ssm_api.cpp", "kda_conv.hip", "kda_scan.hip", "kda_scan_tokens.hip"]
 HEADERS = ["kda_internal.h", "kda_device.h", "kda_recurrence_core.h", "kda_producer.h",
-           "kda_ops_internal.h", "kda_linear_core.h"]
+           "kda_ops_internal.h", "kda_linear_core.h", "kda_checks.h", "kda_ssm_internal.h",
+           "kda_ssm_device.h"]
 
 FLAGS = [
     "--offload-arch=gfx950",

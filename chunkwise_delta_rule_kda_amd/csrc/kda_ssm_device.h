@@ -1,0 +1,68 @@
+// Device helpers of the short convolution and the selective scan.
+#pragma once
+
+#include "kda_device.h"
+#include "kda_ssm_internal.h"
+
+namespace kda {
+
+// The sequence that slot w belongs to where sequence n has the slots from cu[n] / len + n on:
+// the last n with cu[n] / len + n <= w, 64 candidates at a time. w is uniform over the wave.
+__device__ __forceinline__ int64_t find_sequence(const int64_t* cu, int64_t n, int64_t len,
+                                                 int64_t w) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, size = n;
+  while (size > 1) {
+    const int64_t step = (size + 63) / 64;
+    const int64_t at = lo + lane * step;
+    const bool ok = lane * step < size && cu[at] / len + at <= w;
+    const int c = __popcll(__ballot(ok));
+    const int64_t skip = (c > 0 ? c - 1 : 0) * step;
+    lo += skip;
+    size = size - skip < step ? size - skip : step;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float load_state(const StateSlots& s, int64_t at) {
+  return s.bf16 ? load1<true>(s.in, at) : load1<false>(s.in, at);
+}
+
+__device__ __forceinline__ void store_state(const StateSlots& s, int64_t at, float x) {
+  if (s.bf16) static_cast<unsigned short*>(s.out)[at] = float_to_bf16_bits(x);
+  else static_cast<float*>(s.out)[at] = x;
+}
+
+// Elements of a sequence's slot for reading or writing; negative where it has none.
+__device__ __forceinline__ int64_t slot_in(const StateSlots& s, int64_t n) {
+  const int64_t i = s.in_idx ? s.in_idx[n] : n;
+  return s.in && i >= 0 && i < s.slots ? i * s.pitch : -1;
+}
+__device__ __forceinline__ int64_t slot_out(const StateSlots& s, int64_t n) {
+  const int64_t i = s.out_idx ? s.out_idx[n] : n;
+  return s.out && i >= 0 && i < s.slots ? i * s.pitch : -1;
+}
+
+// x / (1 + exp(-x))
+__device__ __forceinline__ float siluf_(float x) { return x * sigmoidf_(x); }
+
+constexpr float kLog2e = 1.44269504088896341f;
+
+// log(1 + exp(x)) = max(x, 0) + log(1 + e), e = exp(-|x|), with
+// log(1 + e) = 2 atanh(t) = 2 t (1 + t^2 / 3 + t^4 / 5 + ...), t = e / (2 + e) <= 1/3: the
+// first term left out is 1.4e-8 of the sum. A logarithm of the rounded 1 + e would lose
+// all digits of the small step sizes.
+__device__ __forceinline__ float softplusf_(float x) {
+  const float e = __builtin_amdgcn_exp2f(-kLog2e * fabsf(x));
+  const float t = e * __builtin_amdgcn_rcpf(2.f + e);
+  const float s = t * t;
+  float r = __builtin_fmaf(s, 1.f / 13, 1.f / 11);
+  r = __builtin_fmaf(s, r, 1.f / 9);
+  r = __builtin_fmaf(s, r, 1.f / 7);
+  r = __builtin_fmaf(s, r, 1.f / 5);
+  r = __builtin_fmaf(s, r, 1.f / 3);
+  r = __builtin_fmaf(s, r, 1.f);
+  return fmaxf(x, 0.f) + 2.f * t * r;
+}
+
+}  // namespace kda

@@ -44,8 +44,10 @@
  *
  * Beside kda_prefill, under the same rules of ownership, errors and indexing: kda_linear
  * (linear attention with one decay per head), kda_pool_copy and kda_pool_compact (slots of
- * a state pool) and kda_gated_norm (the norm behind an attention output or between two
- * blocks); see their sections below.
+ * a state pool), kda_gated_norm (the norm behind an attention output or between two
+ * blocks), kda_short_conv (the causal convolution in front of a recurrence) and
+ * kda_selective_scan (the recurrence with one decay per channel and state); see their
+ * sections below.
  */
 #ifndef KDA_H
 #define KDA_H
@@ -549,6 +551,134 @@ typedef struct kda_gated_norm_args {
 } kda_gated_norm_args;
 kda_status kda_gated_norm_check(const kda_gated_norm_args *a);
 kda_status kda_gated_norm(const kda_gated_norm_args *a, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Short causal convolution
+ *
+ * Each channel with W taps of its own, over each sequence's tokens:
+ *
+ *     y_t[c] = act(bias[c] + sum_i weight[c][i] x_{t - (W-1) + i}[c]),  i = 0 .. W-1
+ *
+ * in FP32, rounded once. The rows before a sequence's first token are its state, the last
+ * W - 1 inputs in front of it, the oldest first; the state behind it is returned. It is what
+ * q, k and v pass before kda_prefill, and u before kda_selective_scan; any T, from one token
+ * on, in one launch without workspace.
+ */
+enum {
+  KDA_CONV_SILU = 1 << 0 /* act is x sigmoid(x); otherwise the identity */
+};
+
+typedef struct kda_short_conv_args {
+  /* Device, read only. x: [B, T, C] of io_dtype, channels contiguous, the others by
+     x_stride. weight: FP32 [C, W]; bias: FP32 [C] or NULL (0). */
+  const void *x;
+  const float *weight, *bias;
+  /* [N, W - 1, C] of state_dtype, or NULL for zeros. */
+  const void *state_in;
+  /* int64 [N + 1] packed-varlen offsets (B must be 1), or NULL; as in kda_prefill_args. */
+  const int64_t *cu_seqlens;
+
+  /* Outputs (device). out: contiguous [B, T, C] of io_dtype, must not overlap any input.
+     state_out: [N, W - 1, C] of state_dtype, or NULL; may be exactly state_in. */
+  void *out;
+  void *state_out;
+
+  int64_t B, T, C, W, N; /* C a multiple of 8 up to 2^24; W 2, 3 or 4 */
+  int64_t x_stride[2];   /* batch, token in elements; not negative, multiples of 8 */
+  int32_t io_dtype;      /* kda_dtype of x and out */
+  int32_t state_dtype;   /* kda_dtype of state_in and state_out */
+  int32_t flags;         /* KDA_CONV_* */
+
+  /* State pool: as in kda_linear_args. */
+  const int32_t *ssm_state_indices;
+  const int32_t *state_out_indices;
+  int64_t state_pool_slots;
+  int64_t state_slot_pitch; /* elements between slots (0 = (W - 1) * C); a multiple of 8 */
+} kda_short_conv_args;
+/* Every check kda_short_conv does (host only). */
+kda_status kda_short_conv_check(const kda_short_conv_args *a);
+/* Enqueue on `stream` (a hipStream_t of the current device). Asynchronous, allocates
+   nothing, may be captured. */
+kda_status kda_short_conv(const kda_short_conv_args *a, void *stream);
+
+/* ------------------------------------------------------------------------------------
+ * Selective state space scan
+ *
+ * For every sequence and channel c with its S states h, starting from state_in (or zeros),
+ * every token t updates
+ *
+ *     d = softplus(delta_t[c] + delta_bias[c])
+ *     h[s] <- exp(d A[c][s]) h[s] + d u_t[c] B_t[s]
+ *     out_t[c] = (sum_s C_t[s] h[s] + D_skip[c] u_t[c]) * z_t[c] sigmoid(z_t[c])
+ *
+ * in FP32, out rounded once, and the final h is written to state_out. Channel c reads rows
+ * c / (D / G) of B and C. A is meant to be finite and negative. 1 <= T <= 8 tokens in the
+ * fixed layout (automatic geometry) run the token form: one read and one write of each
+ * state, no workspace.
+ */
+enum {
+  KDA_SCAN_SOFTPLUS = 1 << 0 /* otherwise d = delta + delta_bias as it is */
+};
+
+typedef struct kda_selective_scan_args {
+  /* Inputs (device, read only). u, delta, z: [B, T, D] of io_dtype, channels contiguous, the
+     others by the strides below; z may be NULL (no gate). B_in, C_in: [B, T, G, S] of
+     io_dtype, S contiguous. A: FP32 [D, S]; D_skip, delta_bias: FP32 [D] or NULL (0). */
+  const void *u, *delta, *z, *B_in, *C_in;
+  const float *A, *D_skip, *delta_bias;
+  /* [N, D, S] of state_dtype, or NULL for a zero initial state. */
+  const void *state_in;
+  /* int64 [N + 1] packed-varlen offsets (B must be 1), or NULL; as in kda_prefill_args. */
+  const int64_t *cu_seqlens;
+
+  /* Outputs (device). out: contiguous [B, T, D] of io_dtype, must not overlap any input.
+     state_out: [N, D, S] of state_dtype, or NULL; may be exactly state_in. */
+  void *out;
+  void *state_out;
+
+  /* Caller-owned scratch of kda_selective_scan_workspace_bytes() bytes, 256-byte aligned;
+     may be NULL when that is 0. Nothing in it needs clearing; two calls that overlap in time
+     (also as replays of two captured graphs) need one each. */
+  void *workspace;
+  size_t workspace_bytes;
+
+  int64_t B, T, D, S, G, N; /* D a multiple of 8 up to 2^22; S 8, 16, 32 or 64; G divides D,
+                               groups of a multiple of 32 channels unless G is 1 */
+  /* Strides in elements: batch, token (and group). Not negative, multiples of 8. */
+  int64_t u_stride[2], delta_stride[2], z_stride[2], B_stride[3], C_stride[3];
+  int32_t io_dtype;    /* kda_dtype of u, delta, z, B_in, C_in and out */
+  int32_t state_dtype; /* kda_dtype of state_in and state_out */
+  int32_t flags;       /* KDA_SCAN_* */
+
+  /* Time segments: tokens per segment (a positive multiple of 64), 0 = automatic,
+     negative = one serial run per sequence. With segments, their end states are formed
+     first, in parallel, then all outputs, in parallel, each from the ends before it. Results
+     differ from the serial form only by rounding. */
+  int64_t segment_tokens;
+
+  /* State pool: as in kda_linear_args. */
+  const int32_t *ssm_state_indices;
+  const int32_t *state_out_indices;
+  int64_t state_pool_slots;
+  int64_t state_slot_pitch; /* elements between slots (0 = D * S); a multiple of 8 */
+} kda_selective_scan_args;
+
+typedef struct kda_selective_scan_plan_info {
+  int32_t decode;          /* 1: the token form */
+  int64_t segment_tokens;  /* 0: serial form */
+  int64_t segments_bound;  /* bound on the number of segments (0 in the serial form) */
+  int64_t workgroups;      /* of the launch that writes out */
+  size_t workspace_bytes;
+} kda_selective_scan_plan_info;
+
+/* Host only, no HIP call: sizes and geometry / every check kda_selective_scan does. */
+kda_status kda_selective_scan_workspace_bytes(const kda_selective_scan_args *a, size_t *bytes);
+kda_status kda_selective_scan_check(const kda_selective_scan_args *a);
+kda_status kda_selective_scan_plan(const kda_selective_scan_args *a,
+                                   kda_selective_scan_plan_info *out);
+/* Enqueue on `stream` (a hipStream_t of the current device). Asynchronous, allocates
+   nothing, may be captured. */
+kda_status kda_selective_scan(const kda_selective_scan_args *a, void *stream);
 
 int32_t kda_abi_version(void);
 

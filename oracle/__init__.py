@@ -26,6 +26,7 @@ Modules
                 The gate formula is not printed on the pages: parity unpinned against
                 the pages for ``safe_gate`` (only its range and special case are pinned).
 ``linear``      linear attention with one decay per head, pool compaction, gated norm.
+``ssm``         the short causal convolution and the selective state space scan.
 """
 
 from .kda_token import checkpoint_starts, kda_recurrence_fp64, token_step
@@ -37,6 +38,7 @@ from .kda_chunk import (
     inverse_neumann,
 )
 from .linear import compact_slots, gated_norm_fp64, linear_recurrence_fp64
+from .ssm import selective_scan_fp64, short_conv_fp64
 from .transforms import l2_normalize, sigmoid, safe_gate
 
 __all__ = [
@@ -54,4 +56,6 @@ __all__ = [
     "linear_recurrence_fp64",
     "compact_slots",
     "gated_norm_fp64",
+    "selective_scan_fp64",
+    "short_conv_fp64",
 ]
