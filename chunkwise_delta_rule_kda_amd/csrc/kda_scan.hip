@@ -4,11 +4,11 @@
 // time by channel, so nothing of it is a matrix product: per (token, channel, state) it is two
 // multiplications, an exponential and two fused multiply-adds of the vector units.
 //
-// A workgroup holds 32 channels of one sequence (or of one time segment of it), a wave eight
-// of them: lane L has channel L % 8 and the n / 8 states of group L / 8, in registers for the
-// whole run. Tiles of 32 tokens go through LDS twice buffered, with one barrier each: all
-// threads bring u, delta and B, C from memory two tiles ahead and turn delta into d and d u,
-// and finish the outputs of the tile before.
+// A workgroup has 32 channels of one sequence (or of one time segment of it). Four waves hold
+// the states of eight channels each: lane L has channel L % 8 and the n / 8 states of group
+// L / 8, in registers for the whole run. Four others bring tiles of 32 tokens through LDS,
+// twice buffered, with one barrier each: u, delta, z, B and C come from memory two tiles ahead,
+// delta becomes d and d u, and the outputs of the tile before are finished.
 
 #include "kda_ssm_device.h"
 
@@ -100,148 +100,40 @@ __device__ __forceinline__ float reduce8(const float (&v)[8]) {
                                               0, __builtin_bit_cast(int, give), 0x128, 0xF, 0xF, false));  // row_ror 8
 }
 
-constexpr int kYRow = kScanChannels + 8;  // floats of an LDS row of y: no two rows' banks meet
+constexpr int kYRow = kScanChannels + 8;      // floats of an LDS row of y, and of a pair of
+constexpr int kDxRow = 4 * kScanChannels + 4; // tokens' step sizes: no two rows' banks meet
 
-// OUT: outputs from the true start state; otherwise a segment's end state from zero (the
-// first segment's from the sequence's start) and the sum of its step sizes.
-template <bool BF16, int N, bool OUT>
-__global__ __launch_bounds__(256) void scan_kernel(ScanParams p) {
-  constexpr int NS = N / 8;                // states of a lane
-  constexpr int kBC = OUT ? 2 * NS : NS;   // of B and C, for a lane and token
-  constexpr int kQuads = N / 4 * (OUT ? 2 : 1) * kScanTile;  // pieces of four of a tile's B and C
-  constexpr int kPer = (kQuads + 255) / 256;
-  __shared__ float dx[2][kScanTile / 2][kScanChannels][4];  // d, d u of two tokens
-  __shared__ float bc[2][kScanTile][8][kBC];
-  __shared__ float ys[OUT ? 2 : 1][OUT ? kScanTile : 1][kYRow];
+// A tile in LDS.
+template <int N, bool OUT>
+struct ScanTile {
+  static constexpr int kBC = OUT ? N / 4 : N / 8;  // of B and C, for a lane and token
+  float dx[kScanTile / 2][kDxRow];  // [channel][4]: d, d u of two tokens
+  float bc[kScanTile][8][kBC];      // [group]: its B, then its C
+  float y[OUT ? kScanTile : 1][kYRow];
+};
 
-  ScanTask task;
-  if (!scan_task(p, task)) return;
-  if (!OUT && task.last && !task.first) return;  // nobody starts from its end
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int ch = lane & 7, g = lane >> 3;
-  const int64_t c0 = static_cast<int64_t>(task.cblk) * kScanChannels;
+// A lane's states, in the waves that hold them.
+template <int N, bool OUT>
+struct ScanStates {
+  static constexpr int NS = N / 8;
+  float A[NS], h[NS], sum;
 
-  // ---- this lane's channel and states
-  const int64_t c = c0 + 8 * wave + ch;
-  const bool held = c < p.D;
-  float A[NS], h[NS];
-  float sum = 0.f;
-#pragma unroll
-  for (int s = 0; s < NS; ++s) {
-    A[s] = held ? p.A[c * N + g * NS + s] * kLog2e : 0.f;
-    h[s] = 0.f;
-  }
-  const int64_t mine = c * N + g * NS;  // in a slot
-  if (held) {
-    if (p.segmented && OUT) {
-      // the start state, through the ends of the segments before
-      const int64_t base = task.slot - task.seg, all = p.D * N;
-      if (task.first) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) h[s] = p.starts[task.n * all + mine + s];
-      }
-      for (int64_t q = 0; q < task.seg; ++q) {
-        const float d = p.sums[(base + q) * p.D + c];
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-          h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * A[s]), h[s], p.ends[(base + q) * all + mine + s]);
-      }
-    } else if (task.first) {
-      const int64_t in = slot_in(p.state, task.n);
-      if (in >= 0) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) h[s] = load_state(p.state, in + mine + s);
-      }
-      if (!OUT) {
-#pragma unroll
-        for (int s = 0; s < NS; ++s) p.starts[task.n * p.D * N + mine + s] = h[s];
-        if (task.last) return;
-      }
-    }
-  }
-  if (!OUT && task.last) return;
-
-  // ---- what this thread brings of each tile: four channels of a token, pieces of B and C
-  const int tok = tid >> 3, quad = 4 * (tid & 7);
-  const bool loads = c0 + quad < p.D;
-  const int64_t nb = p.cu_seqlens ? 0 : task.n;
-  const int64_t ub = nb * p.us[0] + task.row0 * p.us[1] + c0 + quad;
-  const int64_t db = nb * p.ds[0] + task.row0 * p.ds[1] + c0 + quad;
-  const int64_t zb = nb * p.zs[0] + task.row0 * p.zs[1] + c0 + quad;
-  const int64_t group = c0 / p.per_group;
-  const int64_t bb = nb * p.bs[0] + task.row0 * p.bs[1] + group * p.bs[2];
-  const int64_t cb = nb * p.cs[0] + task.row0 * p.cs[1] + group * p.cs[2];
-  const int64_t ob = (nb * p.T + task.row0) * p.D + c0 + quad;
-  float bias[4], skip[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    bias[e] = loads && p.bias ? p.bias[c0 + quad + e] : 0.f;
-    skip[e] = OUT && loads && p.skip ? p.skip[c0 + quad + e] : 0.f;
-  }
-
-  struct Raw {
-    Raw4<BF16> u, d, z, b[kPer];
-  };
-  auto fetch = [&](int64_t t0, Raw& r) {
-    const int64_t t = t0 + tok;
-    if (loads && t < task.len) {
-      r.u.load(p.u, ub + t * p.us[1]);
-      r.d.load(p.delta, db + t * p.ds[1]);
-      if (OUT && p.z) r.z.load(p.z, zb + t * p.zs[1]);
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int j = tid + 256 * i;
-      // piece j: the token's quads of B, then those of C
-      const int row = j / (kQuads / kScanTile), q = j % (kQuads / kScanTile);
-      const int64_t tt = t0 + row;
-      if (j < kQuads && tt < task.len) {
-        if (q < N / 4) r.b[i].load(p.B, bb + tt * p.bs[1] + 4 * q);
-        else r.b[i].load(p.C, cb + tt * p.cs[1] + 4 * (q - N / 4));
-      } else {
-        r.b[i].clear();
-      }
-    }
-  };
-  auto prepare = [&](int64_t t0, const Raw& r, int buf) {
-    const bool here = loads && t0 + tok < task.len;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float d = r.d[e] + bias[e];
-      if (p.softplus) d = softplusf_(d);
-      float x = d * r.u[e];
-      if (!here) d = x = 0.f;
-      f32x2 pair = {d, x};
-      *reinterpret_cast<f32x2*>(&dx[buf][tok >> 1][quad + e][2 * (tok & 1)]) = pair;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int j = tid + 256 * i;
-      const int row = j / (kQuads / kScanTile), q = j % (kQuads / kScanTile);
-      if (j >= kQuads) continue;
-      const int at = q < N / 4 ? 0 : NS, n0 = q < N / 4 ? 4 * q : 4 * q - N;
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = r.b[i][e];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) bc[buf][row][(n0 + e) / NS][at + (n0 + e) % NS] = v[e];
-    }
-  };
   // Eight tokens of a tile from t8 on (the last ones of a segment may be fewer).
-  auto eight = [&](int buf, int t8, int count) {
+  __device__ __forceinline__ void eight(ScanTile<N, OUT>& tile, int column, int g, int t8, int count) {
+    constexpr int kBC = ScanTile<N, OUT>::kBC;
     float y[8];
 #pragma unroll
     for (int tp = 0; tp < 4; ++tp) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(&dx[buf][t8 / 2 + tp][8 * wave + ch][0]);
+      const f32x4 v = *reinterpret_cast<const f32x4*>(&tile.dx[t8 / 2 + tp][4 * column]);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int t = 2 * tp + j;
         const float d = v[2 * j], x = v[2 * j + 1];
         float r[kBC];
 #pragma unroll
-        for (int e = 0; e < kBC; ++e) r[e] = bc[buf][t8 + t][g][e];
+        for (int e = 0; e < kBC; ++e) r[e] = tile.bc[t8 + t][g][e];
         float acc = 0.f;
-        if (t < count) {  // a token behind the end must not touch the state: 0 A may be NaN
+        if (t < count) {  // what is behind the end must not touch the state
 #pragma unroll
           for (int s = 0; s < NS; ++s) {
             const float a = __builtin_amdgcn_exp2f(d * A[s]);
@@ -253,43 +145,218 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanParams p) {
         y[t] = acc;
       }
     }
-    if constexpr (OUT) ys[buf][t8 + g][8 * wave + ch] = reduce8(y);
+    if constexpr (OUT) tile.y[t8 + g][column] = reduce8(y);
+  }
+
+  __device__ __forceinline__ void run(ScanTile<N, OUT>& tile, int column, int g, int64_t left) {
+    if (left >= kScanTile) {
+#pragma unroll
+      for (int t8 = 0; t8 < kScanTile; t8 += 8) eight(tile, column, g, t8, 8);
+    } else {
+      for (int t8 = 0; t8 < left; t8 += 8)
+        eight(tile, column, g, t8, left - t8 < 8 ? static_cast<int>(left) - t8 : 8);
+    }
+  }
+};
+
+// The waves that bring the tiles and finish the outputs: a thread has four channels of a
+// token, and pieces of four of B and C. Rows and channels behind the end are read as the last
+// ones there are.
+template <bool BF16, int N, bool OUT>
+struct ScanLoader {
+  static constexpr int kRow = N / 4 * (OUT ? 2 : 1);  // pieces of a token's B and C
+  static constexpr int kPieces = kRow * kScanTile, kPer = (kPieces + 255) / 256;
+  static constexpr int kElem = BF16 ? 2 : 4;
+  const ScanParams& p;
+  const int64_t len;
+  const int tok, quad;
+  const char *u, *delta, *z;  // the segment's first row and this workgroup's first channel
+  char* out;
+  const char* piece[kPer];
+  int64_t piece_stride[kPer];
+  int channel;                // of this thread's four, inside D
+  bool held;
+  float bias[4], skip[4];
+
+  struct Raw {
+    Raw4<BF16> u, d, z, b[kPer];
   };
-  auto finish = [&](int64_t t0, const Raw4<BF16>& u, const Raw4<BF16>& z, int buf) {
-    if (!loads || t0 + tok >= task.len) return;
-    const f32x4 y = *reinterpret_cast<const f32x4*>(&ys[buf][tok][quad]);
+
+  __device__ __forceinline__ ScanLoader(const ScanParams& params, const ScanTask& t, int tid)
+      : p(params), len(t.len), tok(tid >> 3), quad(4 * (tid & 7)) {
+    const int64_t c0 = static_cast<int64_t>(t.cblk) * kScanChannels;
+    const int64_t n = p.cu_seqlens ? 0 : t.n;
+    held = c0 + quad < p.D;
+    channel = held ? quad : static_cast<int>(p.D - 4 - c0);
+    u = static_cast<const char*>(p.u) + (n * p.us[0] + t.row0 * p.us[1] + c0) * kElem;
+    delta = static_cast<const char*>(p.delta) + (n * p.ds[0] + t.row0 * p.ds[1] + c0) * kElem;
+    z = static_cast<const char*>(p.z) + (n * p.zs[0] + t.row0 * p.zs[1] + c0) * kElem;
+    out = static_cast<char*>(p.out) + ((n * p.T + t.row0) * p.D + c0) * kElem;
+    const int64_t group = c0 / p.per_group;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int q = (tid + 256 * i) % kRow;
+      const bool is_b = q < N / 4;
+      const int64_t(&st)[3] = is_b ? p.bs : p.cs;
+      piece_stride[i] = st[1] * kElem;
+      piece[i] = static_cast<const char*>(is_b ? p.B : p.C) +
+                 (n * st[0] + t.row0 * st[1] + group * st[2] + 4 * (is_b ? q : q - N / 4)) * kElem;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      bias[e] = p.bias ? p.bias[c0 + channel + e] : 0.f;
+      skip[e] = OUT && p.skip ? p.skip[c0 + channel + e] : 0.f;
+    }
+  }
+
+  // Tile from t0 on, where it has a token.
+  __device__ __forceinline__ void fetch(int64_t t0, int tid, Raw& r) {
+    if (t0 >= len) return;
+    const int last = len - t0 < kScanTile ? static_cast<int>(len - t0) - 1 : kScanTile - 1;
+    const uint32_t row = tok < last ? tok : last;
+    r.u.load(u + t0 * p.us[1] * kElem, row * static_cast<uint32_t>(p.us[1]) + channel);
+    r.d.load(delta + t0 * p.ds[1] * kElem, row * static_cast<uint32_t>(p.ds[1]) + channel);
+    if (OUT && p.z) r.z.load(z + t0 * p.zs[1] * kElem, row * static_cast<uint32_t>(p.zs[1]) + channel);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = tid + 256 * i;
+      if (kPieces % 256 && j >= kPieces) continue;
+      const int of = j / kRow < last ? j / kRow : last;
+      r.b[i].load(piece[i] + (t0 + of) * piece_stride[i], 0);
+    }
+  }
+
+  __device__ __forceinline__ void prepare(int tid, const Raw& r, ScanTile<N, OUT>& tile) {
+    constexpr int NS = N / 8;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float d = r.d[e] + bias[e];
+      if (p.softplus) d = softplusf_(d);
+      const f32x2 pair = {d, d * r.u[e]};
+      *reinterpret_cast<f32x2*>(&tile.dx[tok >> 1][4 * (quad + e) + 2 * (tok & 1)]) = pair;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int j = tid + 256 * i;
+      if (kPieces % 256 && j >= kPieces) continue;
+      const int q = j % kRow;
+      const int at = q < N / 4 ? 0 : NS, n0 = q < N / 4 ? 4 * q : 4 * q - N;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) tile.bc[j / kRow][(n0 + e) / NS][at + (n0 + e) % NS] = r.b[i][e];
+    }
+  }
+
+  __device__ __forceinline__ void finish(int64_t t0, const Raw4<BF16>& ru, const Raw4<BF16>& rz,
+                                         const ScanTile<N, OUT>& tile) {
+    const f32x4 y = *reinterpret_cast<const f32x4*>(&tile.y[OUT ? tok : 0][quad]);
     f32x4 o;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      o[e] = p.skip ? __builtin_fmaf(skip[e], u[e], y[e]) : y[e];
-      if (p.z) o[e] *= siluf_(z[e]);
+      o[e] = p.skip ? __builtin_fmaf(skip[e], ru[e], y[e]) : y[e];
+      if (p.z) o[e] *= siluf_(rz[e]);
     }
-    store4<BF16>(p.out, ob + (t0 + tok) * p.D, o);
-  };
+    if (held && t0 + tok < len)
+      store4<BF16>(out + t0 * p.D * kElem, static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.D) + quad, o);
+  }
+};
 
-  Raw raw[2];
-  fetch(0, raw[0]);
-  fetch(kScanTile, raw[1]);
-  prepare(0, raw[0], 0);
-  meet();
-  auto tile = [&](int64_t t0, int buf) {
-    Raw& r = raw[buf];
-    const Raw4<BF16> u = r.u, z = r.z;
-    fetch(t0 + 2 * kScanTile, r);
-    const int64_t left = task.len - t0;
-    if (left >= kScanTile) {
-#pragma unroll
-      for (int t8 = 0; t8 < kScanTile; t8 += 8) eight(buf, t8, 8);
-    } else {
-      for (int t8 = 0; t8 < left; t8 += 8) eight(buf, t8, left - t8 < 8 ? static_cast<int>(left) - t8 : 8);
-    }
-    prepare(t0 + kScanTile, raw[buf ^ 1], buf ^ 1);
+// OUT: outputs from the true start state; otherwise a segment's end state from zero (the
+// first segment's from the sequence's start) and the sum of its step sizes.
+template <bool BF16, int N, bool OUT>
+__global__ __launch_bounds__(512) void scan_kernel(ScanParams p) {
+  constexpr int NS = N / 8;  // states of a lane
+  __shared__ ScanTile<N, OUT> tiles[2];
+
+  ScanTask task;
+  if (!scan_task(p, task)) return;
+  if (!OUT && task.last && !task.first) return;  // nobody starts from its end
+  const int tid = threadIdx.x & 255;
+
+  if (threadIdx.x >= 256) {
+    // ---- the waves that load and finish
+    using Loader = ScanLoader<BF16, N, OUT>;
+    if (!OUT && task.last) return;
+    Loader load(p, task, tid);
+    typename Loader::Raw raw[2];
+    load.fetch(0, tid, raw[0]);
+    load.fetch(kScanTile, tid, raw[1]);
+    Raw4<BF16> u[2], z[2];  // of the tile being scanned and of the one before
+    u[0] = u[1] = raw[0].u;
+    z[0] = z[1] = raw[0].z;
+    load.prepare(tid, raw[0], tiles[0]);
+    load.fetch(2 * kScanTile, tid, raw[0]);
     meet();
-    if constexpr (OUT) finish(t0, u, z, buf);
-  };
+    auto step = [&](int64_t t0, int buf) {  // while the tile at t0 is scanned
+      if (OUT && t0 > 0) load.finish(t0 - kScanTile, u[1], z[1], tiles[buf ^ 1]);
+      u[1] = u[0];
+      z[1] = z[0];
+      if (t0 + kScanTile < task.len) {
+        u[0] = raw[buf ^ 1].u;
+        z[0] = raw[buf ^ 1].z;
+        load.prepare(tid, raw[buf ^ 1], tiles[buf ^ 1]);
+        load.fetch(t0 + 3 * kScanTile, tid, raw[buf ^ 1]);
+      }
+      meet();
+    };
+    int64_t t0 = 0;
+    for (; t0 < task.len; t0 += 2 * kScanTile) {
+      step(t0, 0);
+      if (t0 + kScanTile < task.len) step(t0 + kScanTile, 1);
+    }
+    if (OUT && task.len > 0) {
+      const int64_t tiles_done = (task.len + kScanTile - 1) / kScanTile;
+      load.finish((tiles_done - 1) * kScanTile, u[1], z[1], tiles[(tiles_done - 1) & 1]);
+    }
+    return;
+  }
+
+  // ---- the waves that hold the states
+  const int lane = tid & 63, ch = lane & 7, g = lane >> 3;
+  const int column = 8 * (tid >> 6) + ch;
+  const int64_t c = static_cast<int64_t>(task.cblk) * kScanChannels + column;
+  const bool held = c < p.D;
+  const int64_t mine = c * N + g * NS;  // in a slot
+  ScanStates<N, OUT> st;
+  st.sum = 0.f;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    st.A[s] = held ? p.A[mine + s] * kLog2e : 0.f;
+    st.h[s] = 0.f;
+  }
+  if (held && p.segmented && OUT) {
+    // the start state, through the ends of the segments before
+    const int64_t base = task.slot - task.seg, all = p.D * N;
+    if (task.first) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) st.h[s] = p.starts[task.n * all + mine + s];
+    }
+    for (int64_t q = 0; q < task.seg; ++q) {
+      const float d = p.sums[(base + q) * p.D + c];
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        st.h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * st.A[s]), st.h[s], p.ends[(base + q) * all + mine + s]);
+    }
+  } else if (held && task.first) {
+    const int64_t in = slot_in(p.state, task.n);
+    if (in >= 0) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) st.h[s] = load_state(p.state, in + mine + s);
+    }
+    if (!OUT) {
+#pragma unroll
+      for (int s = 0; s < NS; ++s) p.starts[task.n * p.D * N + mine + s] = st.h[s];
+    }
+  }
+  if (!OUT && task.last) return;
+
+  meet();
   for (int64_t t0 = 0; t0 < task.len; t0 += 2 * kScanTile) {
-    tile(t0, 0);
-    if (t0 + kScanTile < task.len) tile(t0 + kScanTile, 1);
+    st.run(tiles[0], column, g, task.len - t0);
+    meet();
+    if (t0 + kScanTile < task.len) {
+      st.run(tiles[1], column, g, task.len - t0 - kScanTile);
+      meet();
+    }
   }
 
   if (!held) return;
@@ -297,18 +364,18 @@ __global__ __launch_bounds__(256) void scan_kernel(ScanParams p) {
     const int64_t out = task.last ? slot_out(p.state, task.n) : -1;
     if (out >= 0) {
 #pragma unroll
-      for (int s = 0; s < NS; ++s) store_state(p.state, out + mine + s, h[s]);
+      for (int s = 0; s < NS; ++s) store_state(p.state, out + mine + s, st.h[s]);
     }
   } else {
 #pragma unroll
-    for (int s = 0; s < NS; ++s) p.ends[task.slot * p.D * N + mine + s] = h[s];
-    if (g == 0) p.sums[task.slot * p.D + c] = sum;
+    for (int s = 0; s < NS; ++s) p.ends[task.slot * p.D * N + mine + s] = st.h[s];
+    if (g == 0) p.sums[task.slot * p.D + c] = st.sum;
   }
 }
 
 template <bool OUT, bool BF16>
 hipError_t go(const ScanParams& p, int n, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(scan_grid(p))), block(256);
+  const dim3 grid(static_cast<unsigned>(scan_grid(p))), block(512);
   switch (n) {
     case 8: hipLaunchKernelGGL((scan_kernel<BF16, 8, OUT>), grid, block, 0, stream, p); break;
     case 16: hipLaunchKernelGGL((scan_kernel<BF16, 16, OUT>), grid, block, 0, stream, p); break;

@@ -32,6 +32,8 @@ kda_status strides_shape(const int64_t* st, int n, const char* name) {
   for (int d = 0; d < n; ++d)
     if (st[d] < 0 || st[d] > kBig || st[d] % 8)
       return fail(KDA_ERR_SHAPE, "%s stride %lld is negative or not a multiple of 8", name, (long long)st[d]);
+  if (st[1] > (int64_t(1) << 22))  // a tile's rows stay within 2^31 bytes
+    return fail(KDA_ERR_SHAPE, "%s token stride %lld exceeds 2^22", name, (long long)st[1]);
   return KDA_OK;
 }
 
@@ -127,8 +129,8 @@ kda_status conv_check(const kda_short_conv_args* a, ConvPlan* pl) {
   if (!a) return fail(KDA_ERR_NULL, "args is NULL");
   kda_status s = sequences_shape(a->B, a->T, a->N, a->cu_seqlens);
   if (s != KDA_OK) return s;
-  if (a->C < 8 || a->C > (1 << 24) || a->C % 8)
-    return fail(KDA_ERR_SHAPE, "C=%lld is not a multiple of 8 up to 2^24", (long long)a->C);
+  if (a->C < 8 || a->C > (1 << 22) || a->C % 8)
+    return fail(KDA_ERR_SHAPE, "C=%lld is not a multiple of 8 up to 2^22", (long long)a->C);
   if (a->W < 2 || a->W > 4) return fail(KDA_ERR_SHAPE, "W=%lld, 2 to 4 taps are supported", (long long)a->W);
   if (a->flags & ~KDA_CONV_SILU) return fail(KDA_ERR_FLAGS, "unknown flags 0x%x", a->flags);
   const int64_t dense = (a->W - 1) * a->C;

@@ -583,8 +583,9 @@ typedef struct kda_short_conv_args {
   void *out;
   void *state_out;
 
-  int64_t B, T, C, W, N; /* C a multiple of 8 up to 2^24; W 2, 3 or 4 */
-  int64_t x_stride[2];   /* batch, token in elements; not negative, multiples of 8 */
+  int64_t B, T, C, W, N; /* C a multiple of 8 up to 2^22; W 2, 3 or 4 */
+  int64_t x_stride[2];   /* batch, token in elements; not negative, multiples of 8, a token
+                            stride of at most 2^22 */
   int32_t io_dtype;      /* kda_dtype of x and out */
   int32_t state_dtype;   /* kda_dtype of state_in and state_out */
   int32_t flags;         /* KDA_CONV_* */
@@ -644,7 +645,8 @@ typedef struct kda_selective_scan_args {
 
   int64_t B, T, D, S, G, N; /* D a multiple of 8 up to 2^22; S 8, 16, 32 or 64; G divides D,
                                groups of a multiple of 32 channels unless G is 1 */
-  /* Strides in elements: batch, token (and group). Not negative, multiples of 8. */
+  /* Strides in elements: batch, token (and group). Not negative, multiples of 8, a token
+     stride of at most 2^22. */
   int64_t u_stride[2], delta_stride[2], z_stride[2], B_stride[3], C_stride[3];
   int32_t io_dtype;    /* kda_dtype of u, delta, z, B_in, C_in and out */
   int32_t state_dtype; /* kda_dtype of state_in and state_out */
