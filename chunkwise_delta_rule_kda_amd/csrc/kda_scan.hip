@@ -118,43 +118,67 @@ struct ScanStates {
   static constexpr int NS = N / 8;
   float A[NS], h[NS], sum;
 
-  // Eight tokens of a tile from t8 on (the last ones of a segment may be fewer).
-  __device__ __forceinline__ void eight(ScanTile<N, OUT>& tile, int column, int g, int t8, int count) {
-    constexpr int kBC = ScanTile<N, OUT>::kBC;
-    float y[8];
+  // What two tokens need from LDS.
+  struct Pair {
+    f32x4 dx;
+    float bc[2][ScanTile<N, OUT>::kBC];
+  };
+  static __device__ __forceinline__ void load(const ScanTile<N, OUT>& tile, int column, int g, int pair, Pair& o) {
+    o.dx = *reinterpret_cast<const f32x4*>(&tile.dx[pair][4 * column]);
 #pragma unroll
-    for (int tp = 0; tp < 4; ++tp) {
-      const f32x4 v = *reinterpret_cast<const f32x4*>(&tile.dx[t8 / 2 + tp][4 * column]);
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int t = 2 * tp + j;
-        const float d = v[2 * j], x = v[2 * j + 1];
-        float r[kBC];
+      for (int e = 0; e < ScanTile<N, OUT>::kBC; ++e) o.bc[j][e] = tile.bc[2 * pair + j][g][e];
+  }
+  __device__ __forceinline__ float token(const Pair& o, int j) {
+    const float d = o.dx[2 * j], x = o.dx[2 * j + 1];
+    const float* r = o.bc[j];
+    float y = 0.f;
 #pragma unroll
-        for (int e = 0; e < kBC; ++e) r[e] = tile.bc[t8 + t][g][e];
-        float acc = 0.f;
-        if (t < count) {  // what is behind the end must not touch the state
-#pragma unroll
-          for (int s = 0; s < NS; ++s) {
-            const float a = __builtin_amdgcn_exp2f(d * A[s]);
-            h[s] = __builtin_fmaf(a, h[s], x * r[s]);
-            if constexpr (OUT) acc = s == 0 ? h[s] * r[NS] : __builtin_fmaf(h[s], r[NS + s], acc);
-          }
-          if constexpr (!OUT) sum += d;
-        }
-        y[t] = acc;
-      }
+    for (int s = 0; s < NS; ++s) {
+      const float a = __builtin_amdgcn_exp2f(d * A[s]);
+      h[s] = __builtin_fmaf(a, h[s], x * r[s]);
+      if constexpr (OUT) y = s == 0 ? h[s] * r[NS] : __builtin_fmaf(h[s], r[NS + s], y);
     }
-    if constexpr (OUT) tile.y[t8 + g][column] = reduce8(y);
+    if constexpr (!OUT) sum += d;
+    return y;
   }
 
   __device__ __forceinline__ void run(ScanTile<N, OUT>& tile, int column, int g, int64_t left) {
+    constexpr int kPairs = kScanTile / 2;
     if (left >= kScanTile) {
+      // LDS is read some tokens ahead; the compiler by itself would read just before the use
+      constexpr int kAhead = NS <= 2 ? 4 : NS == 4 ? 2 : 1;
+      Pair o[kPairs];
+      float y[8];
 #pragma unroll
-      for (int t8 = 0; t8 < kScanTile; t8 += 8) eight(tile, column, g, t8, 8);
-    } else {
-      for (int t8 = 0; t8 < left; t8 += 8)
-        eight(tile, column, g, t8, left - t8 < 8 ? static_cast<int>(left) - t8 : 8);
+      for (int i = 0; i < kAhead; ++i) load(tile, column, g, i, o[i]);
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        if (i + kAhead < kPairs) load(tile, column, g, i + kAhead, o[i + kAhead]);
+        __builtin_amdgcn_sched_barrier(0x407);  // arithmetic may pass
+        y[2 * i % 8] = token(o[i], 0);
+        y[2 * i % 8 + 1] = token(o[i], 1);
+        if constexpr (OUT) {
+          if (i % 4 == 3) tile.y[2 * i - 6 + g][column] = reduce8(y);
+        }
+      }
+      return;
+    }
+    // the last tokens of a segment: what is behind the end must not touch the state
+    for (int t8 = 0; t8 < left; t8 += 8) {
+      float y[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) {
+        Pair o;
+        if (t8 + t < left) {
+          load(tile, column, g, (t8 + t) / 2, o);
+          y[t] = token(o, t & 1);
+        } else {
+          y[t] = 0.f;
+        }
+      }
+      if constexpr (OUT) tile.y[t8 + g][column] = reduce8(y);
     }
   }
 };
