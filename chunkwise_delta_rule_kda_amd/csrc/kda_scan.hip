@@ -26,6 +26,20 @@ struct ScanTask {
   bool first, last;
 };
 
+// The sequence of rank `rank` by decreasing length (in tiles); n at most 64, one for each lane.
+__device__ __forceinline__ int by_length(const int64_t* cu, int n, int rank) {
+  const int lane = threadIdx.x & 63;
+  int64_t len = -1;
+  if (lane < n) len = cu[lane + 1] - cu[lane];
+  const int tiles = static_cast<int>((len + kScanTile - 1) / kScanTile);
+  int mine = 0;
+  for (int j = 0; j < n; ++j) {
+    const int other = __builtin_amdgcn_readlane(tiles, j);
+    mine += other > tiles || (other == tiles && j < lane);
+  }
+  return __builtin_ctzll(__ballot(lane < n && mine == rank));
+}
+
 // Workgroups b and b + 8 run on the same XCD one after the other: they get neighbouring
 // channel blocks, whose 64-byte parts of a BF16 row share a cache line.
 __device__ __forceinline__ bool scan_task(const ScanParams& p, ScanTask& t) {
@@ -38,10 +52,11 @@ __device__ __forceinline__ bool scan_task(const ScanParams& p, ScanTask& t) {
   t.slot = w;
   int64_t total = p.T;
   if (p.cu_seqlens) {
-    t.n = find_sequence(p.cu_seqlens, p.N, p.seg_len, w);
+    t.n = p.longest_first ? by_length(p.cu_seqlens, static_cast<int>(p.N), static_cast<int>(w))
+                          : find_sequence(p.cu_seqlens, p.N, p.seg_len, w);
     t.begin = p.cu_seqlens[t.n];
     total = p.cu_seqlens[t.n + 1] - t.begin;
-    t.seg = w - (t.begin / p.seg_len + t.n);
+    t.seg = p.longest_first ? 0 : w - (t.begin / p.seg_len + t.n);
   } else {
     t.n = w / p.segs_per_seq;
     t.begin = 0;
@@ -56,24 +71,20 @@ __device__ __forceinline__ bool scan_task(const ScanParams& p, ScanTask& t) {
   return true;
 }
 
-// Four consecutive elements as loaded.
+// Four consecutive elements as loaded, `at` bytes from base.
 template <bool BF16>
 struct Raw4 {
   uint32_t x[BF16 ? 2 : 4];
-  __device__ __forceinline__ void load(const void* base, int64_t at) {
+  __device__ __forceinline__ void load(const char* base, uint32_t at) {
     if constexpr (BF16) {
-      const u32x2 w = *reinterpret_cast<const u32x2*>(static_cast<const unsigned short*>(base) + at);
+      const u32x2 w = *reinterpret_cast<const u32x2*>(base + at);
       x[0] = w[0];
       x[1] = w[1];
     } else {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(static_cast<const float*>(base) + at);
+      const u32x4 w = *reinterpret_cast<const u32x4*>(base + at);
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[i] = w[i];
     }
-  }
-  __device__ __forceinline__ void clear() {
-#pragma unroll
-    for (int i = 0; i < (BF16 ? 2 : 4); ++i) x[i] = 0u;
   }
   __device__ __forceinline__ float operator[](int e) const {
     if constexpr (BF16) return __uint_as_float(e % 2 ? x[e / 2] & 0xffff0000u : x[e / 2] << 16);
@@ -81,7 +92,14 @@ struct Raw4 {
   }
 };
 
-// Sums of eight tokens' values over the lane groups L / 8: lane L gets token L / 8's.
+// x of the lanes of a quad that CTRL names, two bits for each of the four.
+template <int CTRL>
+__device__ __forceinline__ float quad_lanes(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, true));
+}
+
+// Sums of eight tokens' values over the eight lanes of a channel, which differ in L % 4 and
+// L / 32: lane L gets token L % 4 + 4 (L / 32)'s.
 __device__ __forceinline__ float reduce8(const float (&v)[8]) {
   float a[4], b[2];
 #pragma unroll
@@ -89,15 +107,11 @@ __device__ __forceinline__ float reduce8(const float (&v)[8]) {
     const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v[i]), __float_as_uint(v[i + 4]), false, false);
     a[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
   }
+  const bool two = threadIdx.x & 2, odd = threadIdx.x & 1;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {  // odd rows of 16 lanes: token i + 2
-    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[i]), __float_as_uint(a[i + 2]), false, false);
-    b[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
-  }
-  const bool odd = threadIdx.x & 8;
-  const float keep = odd ? b[1] : b[0], give = odd ? b[0] : b[1];
-  return keep + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(
-                                              0, __builtin_bit_cast(int, give), 0x128, 0xF, 0xF, false));  // row_ror 8
+  for (int i = 0; i < 2; ++i)  // lanes 2 and 3 of the quad: token i + 2
+    b[i] = (two ? a[i + 2] : a[i]) + quad_lanes<0x4E>(two ? a[i] : a[i + 2]);
+  return (odd ? b[1] : b[0]) + quad_lanes<0xB1>(odd ? b[0] : b[1]);
 }
 
 constexpr int kYRow = kScanChannels + 8;      // floats of an LDS row of y, and of a pair of
@@ -118,65 +132,82 @@ struct ScanStates {
   static constexpr int NS = N / 8;
   float A[NS], h[NS], sum;
 
-  // What two tokens need from LDS.
-  struct Pair {
-    f32x4 dx;
-    float bc[2][ScanTile<N, OUT>::kBC];
-  };
-  static __device__ __forceinline__ void load(const ScanTile<N, OUT>& tile, int column, int g, int pair, Pair& o) {
-    o.dx = *reinterpret_cast<const f32x4*>(&tile.dx[pair][4 * column]);
+  // LDS operands: of a token its row of B and C, of four tokens the step sizes and inputs. The
+  // four lanes of a quad share their channel: each reads one of the four tokens', and the
+  // products take them from their quad.
+  static __device__ __forceinline__ void load_bc(const ScanTile<N, OUT>& tile, int g, int t, float (&r)[ScanTile<N, OUT>::kBC]) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int e = 0; e < ScanTile<N, OUT>::kBC; ++e) o.bc[j][e] = tile.bc[2 * pair + j][g][e];
+    for (int e = 0; e < ScanTile<N, OUT>::kBC; ++e) r[e] = tile.bc[t][g][e];
   }
-  __device__ __forceinline__ float token(const Pair& o, int j) {
-    const float d = o.dx[2 * j], x = o.dx[2 * j + 1];
-    const float* r = o.bc[j];
+  static __device__ __forceinline__ f32x2 load_dx(const ScanTile<N, OUT>& tile, int column, int t4) {
+    const int t = t4 + (threadIdx.x & 3);
+    return *reinterpret_cast<const f32x2*>(&tile.dx[t / 2][4 * column + 2 * (t & 1)]);
+  }
+  template <int J>
+  __device__ __forceinline__ float token(f32x2 dx, const float (&r)[ScanTile<N, OUT>::kBC]) {
     float y = 0.f;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
-      const float a = __builtin_amdgcn_exp2f(d * A[s]);
-      h[s] = __builtin_fmaf(a, h[s], x * r[s]);
+      const float a = __builtin_amdgcn_exp2f(quad_lanes<0x55 * J>(dx[0]) * A[s]);
+      h[s] = __builtin_fmaf(a, h[s], quad_lanes<0x55 * J>(dx[1]) * r[s]);
       if constexpr (OUT) y = s == 0 ? h[s] * r[NS] : __builtin_fmaf(h[s], r[NS + s], y);
     }
-    if constexpr (!OUT) sum += d;
+    if constexpr (!OUT) sum += quad_lanes<0x55 * J>(dx[0]);
     return y;
   }
 
   __device__ __forceinline__ void run(ScanTile<N, OUT>& tile, int column, int g, int64_t left) {
-    constexpr int kPairs = kScanTile / 2;
     if (left >= kScanTile) {
-      // LDS is read some tokens ahead; the compiler by itself would read just before the use
+      // LDS is read ahead; the compiler by itself would read just before the use
       constexpr int kAhead = NS <= 2 ? 4 : NS == 4 ? 2 : 1;
-      Pair o[kPairs];
-      float y[8];
+      float r[kScanTile][ScanTile<N, OUT>::kBC], y[8];
+      f32x2 dx[kScanTile / 4];
+      dx[0] = load_dx(tile, column, 0);
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) load(tile, column, g, i, o[i]);
+      for (int t = 0; t < kAhead; ++t) load_bc(tile, g, t, r[t]);
 #pragma unroll
-      for (int i = 0; i < kPairs; ++i) {
-        if (i + kAhead < kPairs) load(tile, column, g, i + kAhead, o[i + kAhead]);
-        __builtin_amdgcn_sched_barrier(0x407);  // arithmetic may pass
-        y[2 * i % 8] = token(o[i], 0);
-        y[2 * i % 8 + 1] = token(o[i], 1);
+      for (int t4 = 0; t4 < kScanTile; t4 += 4) {
+        if (t4 + 4 < kScanTile) dx[t4 / 4 + 1] = load_dx(tile, column, t4 + 4);
+#pragma unroll
+        for (int j = 0; j < 4; j += kAhead) {
+          const int t = t4 + j;
+#pragma unroll
+          for (int i = t + kAhead; i < t + 2 * kAhead && i < kScanTile; ++i) load_bc(tile, g, i, r[i]);
+          __builtin_amdgcn_sched_barrier(0);
+          float* out = &y[t % 8];
+          const f32x2 v = dx[t4 / 4];
+          if constexpr (kAhead == 4) {
+            out[0] = token<0>(v, r[t]);
+            out[1] = token<1>(v, r[t + 1]);
+            out[2] = token<2>(v, r[t + 2]);
+            out[3] = token<3>(v, r[t + 3]);
+          } else if constexpr (kAhead == 2) {
+            out[0] = j == 0 ? token<0>(v, r[t]) : token<2>(v, r[t]);
+            out[1] = j == 0 ? token<1>(v, r[t + 1]) : token<3>(v, r[t + 1]);
+          } else {
+            out[0] = j == 0 ? token<0>(v, r[t]) : j == 1 ? token<1>(v, r[t]) : j == 2 ? token<2>(v, r[t]) : token<3>(v, r[t]);
+          }
+        }
         if constexpr (OUT) {
-          if (i % 4 == 3) tile.y[2 * i - 6 + g][column] = reduce8(y);
+          if (t4 % 8) tile.y[t4 - 4 + g][column] = reduce8(y);
         }
       }
       return;
     }
     // the last tokens of a segment: what is behind the end must not touch the state
     for (int t8 = 0; t8 < left; t8 += 8) {
-      float y[8];
+      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int t = 0; t < 8; ++t) {
-        Pair o;
-        if (t8 + t < left) {
-          load(tile, column, g, (t8 + t) / 2, o);
-          y[t] = token(o, t & 1);
-        } else {
-          y[t] = 0.f;
-        }
+      for (int i = 0; i < 8; i += 4) {
+        const int64_t more = left - t8 - i;
+        float r[4][ScanTile<N, OUT>::kBC];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_bc(tile, g, t8 + i + j, r[j]);
+        const f32x2 dx = load_dx(tile, column, t8 + i);
+        if (more > 0) y[i] = token<0>(dx, r[0]);
+        if (more > 1) y[i + 1] = token<1>(dx, r[1]);
+        if (more > 2) y[i + 2] = token<2>(dx, r[2]);
+        if (more > 3) y[i + 3] = token<3>(dx, r[3]);
       }
       if constexpr (OUT) tile.y[t8 + g][column] = reduce8(y);
     }
@@ -184,21 +215,26 @@ struct ScanStates {
 };
 
 // The waves that bring the tiles and finish the outputs: a thread has four channels of a
-// token, and pieces of four of B and C. Rows and channels behind the end are read as the last
-// ones there are.
+// token, and pieces of four of B and C, those of B in the first waves. Rows and channels
+// behind the end are read as the last ones there are: every tile then has the same number of
+// loads, and the wait for one tile's leaves the next one's in flight.
 template <bool BF16, int N, bool OUT>
 struct ScanLoader {
-  static constexpr int kRow = N / 4 * (OUT ? 2 : 1);  // pieces of a token's B and C
-  static constexpr int kPieces = kRow * kScanTile, kPer = (kPieces + 255) / 256;
-  static constexpr int kElem = BF16 ? 2 : 4;
+  static constexpr int kOne = N / 4 * kScanTile;             // pieces of a tile's B
+  static constexpr int kPieces = kOne * (OUT ? 2 : 1), kPer = (kPieces + 255) / 256;
+  static constexpr uint32_t kElem = BF16 ? 2 : 4;
   const ScanParams& p;
   const int64_t len;
-  const int tok, quad;
-  const char *u, *delta, *z;  // the segment's first row and this workgroup's first channel
-  char* out;
+  const int tid, tok, quad;
+  int64_t left;                // tokens from the next tile on, of the last tile at the end
+  int64_t done = -kScanTile;   // the tile to finish: none is when the first one is scanned
+  const char *u, *delta, *z;   // the next tile's first row and this workgroup's first channel
+  char* out;                   // of the tile to finish
   const char* piece[kPer];
-  int64_t piece_stride[kPer];
-  int channel;                // of this thread's four, inside D
+  int64_t piece_stride[kPer];  // bytes
+  uint32_t u_at, delta_at, z_at, out_at, piece_at[kPer];  // this thread's part of a whole tile
+  int64_t z_stride;
+  int channel;                 // the first of this thread's four, inside D
   bool held;
   float bias[4], skip[4];
 
@@ -206,26 +242,28 @@ struct ScanLoader {
     Raw4<BF16> u, d, z, b[kPer];
   };
 
-  __device__ __forceinline__ ScanLoader(const ScanParams& params, const ScanTask& t, int tid)
-      : p(params), len(t.len), tok(tid >> 3), quad(4 * (tid & 7)) {
+  __device__ __forceinline__ ScanLoader(const ScanParams& params, const ScanTask& t, int thread)
+      : p(params), len(t.len), tid(thread), tok(thread >> 3), quad(4 * (thread & 7)), left(t.len) {
     const int64_t c0 = static_cast<int64_t>(t.cblk) * kScanChannels;
     const int64_t n = p.cu_seqlens ? 0 : t.n;
     held = c0 + quad < p.D;
     channel = held ? quad : static_cast<int>(p.D - 4 - c0);
     u = static_cast<const char*>(p.u) + (n * p.us[0] + t.row0 * p.us[1] + c0) * kElem;
     delta = static_cast<const char*>(p.delta) + (n * p.ds[0] + t.row0 * p.ds[1] + c0) * kElem;
-    z = static_cast<const char*>(p.z) + (n * p.zs[0] + t.row0 * p.zs[1] + c0) * kElem;
-    out = static_cast<char*>(p.out) + ((n * p.T + t.row0) * p.D + c0) * kElem;
+    z = p.z ? static_cast<const char*>(p.z) + (n * p.zs[0] + t.row0 * p.zs[1] + c0) * kElem : u;
+    z_stride = p.z ? p.zs[1] : p.us[1];
+    out = static_cast<char*>(p.out) + ((n * p.T + t.row0 - kScanTile) * p.D + c0) * kElem;
+    out_at = (static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.D) + quad) * kElem;
     const int64_t group = c0 / p.per_group;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int q = (tid + 256 * i) % kRow;
-      const bool is_b = q < N / 4;
+      const bool is_b = !OUT || 256 * i + 64 * wave < kOne;
       const int64_t(&st)[3] = is_b ? p.bs : p.cs;
       piece_stride[i] = st[1] * kElem;
-      piece[i] = static_cast<const char*>(is_b ? p.B : p.C) +
-                 (n * st[0] + t.row0 * st[1] + group * st[2] + 4 * (is_b ? q : q - N / 4)) * kElem;
+      piece[i] = static_cast<const char*>(is_b ? p.B : p.C) + (n * st[0] + t.row0 * st[1] + group * st[2]) * kElem;
     }
+    places(kScanTile - 1);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       bias[e] = p.bias ? p.bias[c0 + channel + e] : 0.f;
@@ -233,61 +271,93 @@ struct ScanLoader {
     }
   }
 
-  // Tile from t0 on, where it has a token.
-  __device__ __forceinline__ void fetch(int64_t t0, int tid, Raw& r) {
-    if (t0 >= len) return;
-    const int last = len - t0 < kScanTile ? static_cast<int>(len - t0) - 1 : kScanTile - 1;
+  // Where this thread's parts of a tile are whose last row is `last`.
+  __device__ __forceinline__ void places(int last) {
     const uint32_t row = tok < last ? tok : last;
-    r.u.load(u + t0 * p.us[1] * kElem, row * static_cast<uint32_t>(p.us[1]) + channel);
-    r.d.load(delta + t0 * p.ds[1] * kElem, row * static_cast<uint32_t>(p.ds[1]) + channel);
-    if (OUT && p.z) r.z.load(z + t0 * p.zs[1] * kElem, row * static_cast<uint32_t>(p.zs[1]) + channel);
+    u_at = (row * static_cast<uint32_t>(p.us[1]) + channel) * kElem;
+    delta_at = (row * static_cast<uint32_t>(p.ds[1]) + channel) * kElem;
+    z_at = (row * static_cast<uint32_t>(z_stride) + channel) * kElem;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int j = tid + 256 * i;
-      if (kPieces % 256 && j >= kPieces) continue;
-      const int of = j / kRow < last ? j / kRow : last;
-      r.b[i].load(piece[i] + (t0 + of) * piece_stride[i], 0);
+      const int j = (tid + 256 * i) % kOne;
+      const uint32_t of = j / (N / 4) < last ? j / (N / 4) : last;
+      piece_at[i] = of * static_cast<uint32_t>(piece_stride[i]) + 4 * (j % (N / 4)) * kElem;
     }
   }
 
-  __device__ __forceinline__ void prepare(int tid, const Raw& r, ScanTile<N, OUT>& tile) {
+  // The next tile, or the last one again.
+  __device__ __forceinline__ void fetch(Raw& r) {
+    if (left < kScanTile) places(static_cast<int>(left) - 1);
+    r.u.load(u, u_at);
+    r.d.load(delta, delta_at);
+    if (OUT) r.z.load(z, z_at);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) r.b[i].load(piece[i], piece_at[i]);
+    const int64_t rows = left > kScanTile ? kScanTile : 0;
+    left -= rows;
+    u += p.us[1] * rows * kElem;
+    delta += p.ds[1] * rows * kElem;
+    z += z_stride * rows * kElem;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) piece[i] += piece_stride[i] * rows;
+  }
+
+  __device__ __forceinline__ void prepare(const Raw& r, ScanTile<N, OUT>& tile) {
     constexpr int NS = N / 8;
+    float d[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[e] = r.d[e] + bias[e];
+    if (p.softplus) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = softplusf_(d[e]);
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float d = r.d[e] + bias[e];
-      if (p.softplus) d = softplusf_(d);
-      const f32x2 pair = {d, d * r.u[e]};
+      const f32x2 pair = {d[e], d[e] * r.u[e]};
       *reinterpret_cast<f32x2*>(&tile.dx[tok >> 1][4 * (quad + e) + 2 * (tok & 1)]) = pair;
     }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      const int j = tid + 256 * i;
-      if (kPieces % 256 && j >= kPieces) continue;
-      const int q = j % kRow;
-      const int at = q < N / 4 ? 0 : NS, n0 = q < N / 4 ? 4 * q : 4 * q - N;
+      if (kPieces % 256 && tid + 256 * i >= kPieces) continue;
+      const int j = (tid + 256 * i) % kOne, row = j / (N / 4), n0 = 4 * (j % (N / 4));
+      const int at = tid + 256 * i < kOne ? 0 : NS;
+      const Raw4<BF16>& v = r.b[i];
+      if constexpr (NS == 1) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) tile.bc[j / kRow][(n0 + e) / NS][at + (n0 + e) % NS] = r.b[i][e];
+        for (int e = 0; e < 4; ++e) tile.bc[row][n0 + e][at] = v[e];
+      } else if constexpr (NS == 2) {
+#pragma unroll
+        for (int e = 0; e < 4; e += 2)
+          *reinterpret_cast<f32x2*>(&tile.bc[row][(n0 + e) / 2][at]) = f32x2{v[e], v[e + 1]};
+      } else {
+        *reinterpret_cast<f32x4*>(&tile.bc[row][n0 / NS][at + n0 % NS]) = f32x4{v[0], v[1], v[2], v[3]};
+      }
     }
   }
 
-  __device__ __forceinline__ void finish(int64_t t0, const Raw4<BF16>& ru, const Raw4<BF16>& rz,
+  // The outputs of the tile behind the one finished before.
+  __device__ __forceinline__ void finish(const Raw4<BF16>& ru, const Raw4<BF16>& rz,
                                          const ScanTile<N, OUT>& tile) {
-    const f32x4 y = *reinterpret_cast<const f32x4*>(&tile.y[OUT ? tok : 0][quad]);
-    f32x4 o;
+    f32x4 o = *reinterpret_cast<const f32x4*>(&tile.y[OUT ? tok : 0][quad]);
+    if (p.skip) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      o[e] = p.skip ? __builtin_fmaf(skip[e], ru[e], y[e]) : y[e];
-      if (p.z) o[e] *= siluf_(rz[e]);
+      for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(skip[e], ru[e], o[e]);
     }
-    if (held && t0 + tok < len)
-      store4<BF16>(out + t0 * p.D * kElem, static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.D) + quad, o);
+    if (p.z) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] *= siluf_(rz[e]);
+    }
+    if (held && done >= 0 && done + tok < len) store4<BF16>(out + out_at, 0, o);
+    done += kScanTile;
+    out += p.D * (kScanTile * kElem);
   }
 };
 
 // OUT: outputs from the true start state; otherwise a segment's end state from zero (the
 // first segment's from the sequence's start) and the sum of its step sizes.
 template <bool BF16, int N, bool OUT>
-__global__ __launch_bounds__(512) void scan_kernel(ScanParams p) {
+__global__ __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(BF16 && N <= 16 ? 6 : 4))) void
+scan_kernel(ScanParams p) {
   constexpr int NS = N / 8;  // states of a lane
   __shared__ ScanTile<N, OUT> tiles[2];
 
@@ -300,42 +370,41 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanParams p) {
     // ---- the waves that load and finish
     using Loader = ScanLoader<BF16, N, OUT>;
     if (!OUT && task.last) return;
+    if (task.len == 0) {
+      meet();
+      return;
+    }
     Loader load(p, task, tid);
     typename Loader::Raw raw[2];
-    load.fetch(0, tid, raw[0]);
-    load.fetch(kScanTile, tid, raw[1]);
-    Raw4<BF16> u[2], z[2];  // of the tile being scanned and of the one before
+    load.fetch(raw[0]);
+    load.fetch(raw[1]);
+    Raw4<BF16> u[2], z[2];  // of the tile to be scanned next and of the one before
     u[0] = u[1] = raw[0].u;
     z[0] = z[1] = raw[0].z;
-    load.prepare(tid, raw[0], tiles[0]);
-    load.fetch(2 * kScanTile, tid, raw[0]);
+    load.prepare(raw[0], tiles[0]);
+    load.fetch(raw[0]);
     meet();
-    auto step = [&](int64_t t0, int buf) {  // while the tile at t0 is scanned
-      if (OUT && t0 > 0) load.finish(t0 - kScanTile, u[1], z[1], tiles[buf ^ 1]);
+    auto step = [&](int buf) {  // while tiles[buf] is scanned
+      if (OUT) load.finish(u[1], z[1], tiles[buf ^ 1]);
       u[1] = u[0];
       z[1] = z[0];
-      if (t0 + kScanTile < task.len) {
-        u[0] = raw[buf ^ 1].u;
-        z[0] = raw[buf ^ 1].z;
-        load.prepare(tid, raw[buf ^ 1], tiles[buf ^ 1]);
-        load.fetch(t0 + 3 * kScanTile, tid, raw[buf ^ 1]);
-      }
+      u[0] = raw[buf ^ 1].u;
+      z[0] = raw[buf ^ 1].z;
+      load.prepare(raw[buf ^ 1], tiles[buf ^ 1]);
+      load.fetch(raw[buf ^ 1]);
       meet();
     };
-    int64_t t0 = 0;
-    for (; t0 < task.len; t0 += 2 * kScanTile) {
-      step(t0, 0);
-      if (t0 + kScanTile < task.len) step(t0 + kScanTile, 1);
+    for (int64_t t0 = 0; t0 < task.len; t0 += 2 * kScanTile) {
+      step(0);
+      if (t0 + kScanTile >= task.len) break;
+      step(1);
     }
-    if (OUT && task.len > 0) {
-      const int64_t tiles_done = (task.len + kScanTile - 1) / kScanTile;
-      load.finish((tiles_done - 1) * kScanTile, u[1], z[1], tiles[(tiles_done - 1) & 1]);
-    }
+    if (OUT) load.finish(u[1], z[1], tiles[(task.len - 1) / kScanTile & 1]);
     return;
   }
 
   // ---- the waves that hold the states
-  const int lane = tid & 63, ch = lane & 7, g = lane >> 3;
+  const int lane = tid & 63, ch = lane >> 2 & 7, g = (lane & 3) + 4 * (lane >> 5);
   const int column = 8 * (tid >> 6) + ch;
   const int64_t c = static_cast<int64_t>(task.cblk) * kScanChannels + column;
   const bool held = c < p.D;
@@ -354,11 +423,23 @@ __global__ __launch_bounds__(512) void scan_kernel(ScanParams p) {
 #pragma unroll
       for (int s = 0; s < NS; ++s) st.h[s] = p.starts[task.n * all + mine + s];
     }
-    for (int64_t q = 0; q < task.seg; ++q) {
-      const float d = p.sums[(base + q) * p.D + c];
+    constexpr int kBatch = NS <= 2 ? 8 : 2;  // read together: the chain through them is short
+    for (int64_t q0 = 0; q0 < task.seg; q0 += kBatch) {
+      float d[kBatch], e[kBatch][NS];
 #pragma unroll
-      for (int s = 0; s < NS; ++s)
-        st.h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d * st.A[s]), st.h[s], p.ends[(base + q) * all + mine + s]);
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t q = base + (q0 + i < task.seg ? q0 + i : task.seg - 1);
+        d[i] = p.sums[q * p.D + c];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) e[i][s] = p.ends[q * all + mine + s];
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (q0 + i >= task.seg) break;
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          st.h[s] = __builtin_fmaf(__builtin_amdgcn_exp2f(d[i] * st.A[s]), st.h[s], e[i][s]);
+      }
     }
   } else if (held && task.first) {
     const int64_t in = slot_in(p.state, task.n);

@@ -188,7 +188,48 @@ ScanPlan scan_plan(const kda_selective_scan_args* a) {
     pl.tokens = true;
     return pl;
   }
+  // The geometry: the cheapest by a model of the time, in microseconds, fitted to one MI355X,
+  // where a step is a tile of 32 tokens. S = 16, BF16: a workgroup alone on its compute unit
+  // takes 1.25 a step, several 1.04 each; with S it is 0.5 + 0.047 S and 0.4 + 0.04 S, FP32
+  // 0.15 more. The end states take 0.7 of the outputs' time. Serial: the longest sequence's
+  // steps, or all workgroups' over 256 compute units. Segments: two launches of all of them
+  // (8, and 0.2 for each segment whose end a start state has to come through).
+  // One sequence of 8192 tokens, S = 16: D = 768 314 serial, 56 by segments of 256 or 384, 64
+  // by 832; D = 1536 316, 95 (384, 512), 104 (832); D = 4096 320, 227 (512), 242 (1664); D =
+  // 8192 322, 394 by two segments. T = 512, D = 1536: 23.5 serial, 17.8 by segments of 64.
+  const bool bf16 = a->io_dtype == KDA_BF16;
+  const double states = static_cast<double>(a->S);
+  const double alone = 0.5 + 0.047 * states + (bf16 ? 0 : 0.15), shared = 0.4 + 0.04 * states + (bf16 ? 0 : 0.15);
+  const int64_t wgs = a->N * pl.cblocks;
+  // a launch of n workgroups, per step of theirs
+  auto launch = [&](double n) {
+    const double each = n / 256;
+    return each <= 1 ? alone : std::fmax(alone, shared * (each < 4 ? std::ceil(each) : each));
+  };
+  const double steps = static_cast<double>(a->T) / kda::kScanTile;
+  double best;
+  if (a->cu_seqlens && a->N > 1) {
+    // the lengths are not known here: the longest one is taken for 1.75 times the mean
+    const double longest = steps * std::fmin(1.0, 1.75 / static_cast<double>(a->N));
+    best = std::fmax(longest * alone, steps * static_cast<double>(pl.cblocks) / 256 * shared);
+  } else {
+    best = steps * launch(static_cast<double>(wgs));
+  }
   int64_t seg = 0;
+  for (int64_t parts = 2; a->segment_tokens == 0 && parts <= 64; ++parts) {
+    const int64_t len = ceil_div(ceil_div(a->T, parts), 64) * 64;
+    if (len >= a->T) continue;
+    const double n = a->cu_seqlens ? static_cast<double>(ceil_div(a->T, len) + a->N / 2) * static_cast<double>(pl.cblocks)
+                                   : static_cast<double>(ceil_div(a->T, len) * wgs);
+    const double mean = a->cu_seqlens ? static_cast<double>(a->T / a->N) : static_cast<double>(a->T);
+    const double chain = std::fmin(static_cast<double>(parts), 1.75 * mean / static_cast<double>(len));
+    const double time = 8 + 0.2 * chain + static_cast<double>(len / kda::kScanTile) *
+                                              (0.7 * launch(n - static_cast<double>(wgs)) + launch(n));
+    if (1.05 * time < best) {  // two launches and a workspace have to save 5 %
+      best = 1.05 * time;
+      seg = len;
+    }
+  }
   if (a->segment_tokens > 0) seg = a->segment_tokens;
   if (seg >= a->T) seg = 0;
   pl.seg = seg;
@@ -388,6 +429,7 @@ kda_status kda_selective_scan(const kda_selective_scan_args* a, void* stream_) {
   p.slots = pl.slots;
   p.cblocks = pl.cblocks;
   p.segmented = pl.seg ? 1 : 0;
+  p.longest_first = a->cu_seqlens && !pl.seg && a->N > 1 && a->N <= 64;
   unsigned char* ws = static_cast<unsigned char*>(a->workspace);
   p.ends = reinterpret_cast<float*>(ws);
   p.sums = reinterpret_cast<float*>(ws + pl.sums);

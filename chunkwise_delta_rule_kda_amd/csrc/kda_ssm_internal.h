@@ -63,6 +63,7 @@ struct ScanParams {
   int64_t seg_len, segs_per_seq, slots;
   int64_t cblocks;           // workgroups (channel blocks) of a slot
   int32_t segmented;
+  int32_t longest_first;     // serial varlen form: workgroups by decreasing sequence length
   float* ends;               // FP32 [slots][D][n]: a segment's end state
   float* sums;               // FP32 [slots][D]: the sum of its step sizes
   float* starts;             // FP32 [N][D][n]: the sequences' start states
