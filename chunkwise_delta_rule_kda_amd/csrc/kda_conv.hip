@@ -45,17 +45,30 @@ __device__ __forceinline__ void store8(void* base, int64_t at, const float (&y)[
   }
 }
 
-// ROWS: tokens in flight; one for calls of one token each.
-template <bool BF16, int W, int ROWS>
-__global__ __launch_bounds__(256) void conv_kernel(ConvParams p, int64_t octets) {
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t w = item / octets;
-  const int64_t c = 8 * (item - w * octets);
+// LANES octets of channels and 256 / LANES runs for a workgroup; ROWS tokens in flight, one
+// for calls of one token each. The taps come through LDS: read by each thread from memory they
+// would be 64 cache lines a load.
+template <bool BF16, int W, int ROWS, int LANES>
+__global__ __launch_bounds__(256) void conv_kernel(ConvParams p, int64_t blocks) {
+  constexpr int kPitch = 8 * W + 4;  // floats of an octet's taps: sixteen lanes meet all banks
+  __shared__ float taps[LANES * kPitch];
+  const int64_t row = static_cast<int64_t>(blockIdx.x) / blocks;
+  const int64_t octet0 = (blockIdx.x - row * blocks) * LANES;
+  const int lane = threadIdx.x % LANES;
+  const int64_t octets = p.C / 8;
+  const bool held = octet0 + lane < octets;
+  const int64_t c = 8 * (held ? octet0 + lane : octets - 1);
+  const int64_t w = row * (256 / LANES) + threadIdx.x / LANES;
+
+  const int count = static_cast<int>(octets - octet0 < LANES ? octets - octet0 : LANES) * 8 * W;
+  for (int i = 4 * threadIdx.x; i < count; i += 1024)
+    *reinterpret_cast<f32x4*>(&taps[i / (8 * W) * kPitch + i % (8 * W)]) =
+        *reinterpret_cast<const f32x4*>(&p.weight[octet0 * 8 * W + i]);
+
   int64_t n, begin = 0, total = p.T, r;
   if (p.cu_seqlens) {
     // the wave's first lane's sequence, from which the others' are a few further
-    const int64_t first = __shfl(w, 0);
-    n = find_sequence(p.cu_seqlens, p.N, p.run, first);
+    n = find_sequence(p.cu_seqlens, p.N, p.run, __shfl(w, 0));
     while (n + 1 < p.N && p.cu_seqlens[n + 1] / p.run + n + 1 <= w) ++n;
     begin = p.cu_seqlens[n];
     total = p.cu_seqlens[n + 1] - begin;
@@ -64,9 +77,9 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvParams p, int64_t octets)
     n = w / p.runs_per_seq;
     r = w - n * p.runs_per_seq;
   }
-  if (w >= p.slots || r < 0) return;
   const int64_t t0 = r * p.run;
-  if (r > 0 && t0 >= total) return;
+  meet();
+  if (!held || w >= p.slots || r < 0 || (r > 0 && t0 >= total)) return;
   const int64_t len = total - t0 < p.run ? total - t0 : p.run;
   const int64_t xb = (p.cu_seqlens ? 0 : n * p.xs[0]) + begin * p.xs[1] + c;
   const int64_t ob = ((p.cu_seqlens ? 0 : n * p.T) + begin) * p.C + c;
@@ -99,11 +112,14 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvParams p, int64_t octets)
 
   float wt[W][8], bias[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int i = 0; i < 8 * W; i += 4) {
+    const f32x4 v = *reinterpret_cast<const f32x4*>(&taps[lane * kPitch + i]);
 #pragma unroll
-    for (int i = 0; i < W; ++i) wt[i][e] = p.weight[(c + e) * W + i];
-    bias[e] = p.bias ? p.bias[c + e] : 0.f;
+    for (int k = 0; k < 4; ++k) wt[(i + k) % W][(i + k) / W] = v[k];
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bias[e] = 0.f;
+  if (p.bias) load8<false>(p.bias, c, bias);
 
   // The first run's thread writes the final state too: nobody else reads these channels of
   // the initial one, which may be the same memory.
@@ -148,15 +164,21 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvParams p, int64_t octets)
   }
 }
 
+template <bool BF16, int W, int LANES>
+hipError_t go_lanes(const ConvParams& p, hipStream_t stream) {
+  const int64_t blocks = (p.C / 8 + LANES - 1) / LANES, rows = (p.slots * LANES + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(blocks * rows));
+  if (p.T == 1 && !p.cu_seqlens)
+    hipLaunchKernelGGL((conv_kernel<BF16, W, 1, LANES>), grid, dim3(256), 0, stream, p, blocks);
+  else
+    hipLaunchKernelGGL((conv_kernel<BF16, W, kConvRows, LANES>), grid, dim3(256), 0, stream, p, blocks);
+  return hipGetLastError();
+}
+
 template <bool BF16, int W>
 hipError_t go(const ConvParams& p, hipStream_t stream) {
-  const int64_t octets = p.C / 8;
-  const dim3 grid(static_cast<unsigned>((p.slots * octets + 255) / 256));
-  if (p.T == 1 && !p.cu_seqlens)
-    hipLaunchKernelGGL((conv_kernel<BF16, W, 1>), grid, dim3(256), 0, stream, p, octets);
-  else
-    hipLaunchKernelGGL((conv_kernel<BF16, W, kConvRun>), grid, dim3(256), 0, stream, p, octets);
-  return hipGetLastError();
+  return p.lanes == 64 ? go_lanes<BF16, W, 64>(p, stream)
+         : p.lanes == 32 ? go_lanes<BF16, W, 32>(p, stream) : go_lanes<BF16, W, 8>(p, stream);
 }
 
 template <bool BF16>

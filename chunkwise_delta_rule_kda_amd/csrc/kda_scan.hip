@@ -16,9 +16,6 @@ namespace kda {
 
 namespace {
 
-// LDS operations are complete and all waves here; loads from memory stay in flight.
-__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
-
 struct ScanTask {
   int64_t n, slot, row0, len, seg;  // row0: token row of the segment's begin in its sequence's strides
   int64_t begin;                    // first row of the sequence (0 in the fixed layout)

@@ -6,6 +6,9 @@
 
 namespace kda {
 
+// LDS operations are complete and all waves here; loads from memory stay in flight.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
 // The sequence that slot w belongs to where sequence n has the slots from cu[n] / len + n on:
 // the last n with cu[n] / len + n <= w, 64 candidates at a time. w is uniform over the wave.
 __device__ __forceinline__ int64_t find_sequence(const int64_t* cu, int64_t n, int64_t len,

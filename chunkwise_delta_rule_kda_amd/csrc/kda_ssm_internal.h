@@ -18,7 +18,7 @@ struct StateSlots {
   int32_t bf16;
 };
 
-constexpr int kConvRun = 8;  // tokens that a thread of the convolution has in flight
+constexpr int kConvRows = 4;  // tokens that a thread of the convolution has in flight
 
 struct ConvParams {
   const void* x;
@@ -32,6 +32,7 @@ struct ConvParams {
   // belongs to run r of sequence n: w = n * runs_per_seq + r (fixed layout) or
   // cu[n] / run + n + r (varlen).
   int64_t run, runs_per_seq, slots;
+  int32_t lanes;             // octets of channels of a workgroup: 64, 32 or 8
   int32_t silu;
   StateSlots state;
 };
