@@ -95,6 +95,13 @@ def run_on(device, stream):
     return _on(device, stream)
 
 
+def new_state(like, state_in, shape, dtype):
+    """An uninitialised contiguous state."""
+    if state_in is not None:  # checked: contiguous and of that shape and dtype
+        return _torch.empty_like(state_in)
+    return like.new_empty(shape, dtype=dtype)
+
+
 def sequences(cu_seqlens, B):
     """The number of sequences of a call: B, or those that cu_seqlens packs into one row."""
     if cu_seqlens is None:
@@ -119,7 +126,6 @@ def channel_strides(t, name, B, T):
 
 
 def _state_check(t, name, shape, dtype):
-    is_tensor(t, name)
     if t.shape != shape:
         raise KdaError(2, f"{name} has shape {tuple(t.shape)}, expected {shape}")
     if t.dtype != dtype:
@@ -139,14 +145,18 @@ def states(state_in, state_out, state_dtype, io_dtype, N, a, b, ssm_state_indice
     if code == KDA_BF16 and state_dtype != torch.bfloat16:
         raise KdaError(3, f"state dtype {state_dtype}")
     if ssm_state_indices is None:
-        need(state_out_indices is None, 10, "state_out_indices needs ssm_state_indices")
+        if state_out_indices is not None:
+            raise KdaError(10, "state_out_indices needs ssm_state_indices")
+        if state_out is not None:
+            is_tensor(state_out, "state_out")
         for name, t in (("state_in", state_in), ("state_out", state_out)):
             if t is not None:
                 _state_check(t, name, (N, a, b), state_dtype)
                 if not t.is_contiguous():
                     raise KdaError(2, f"{name} must be contiguous")
         return state_out, state_dtype, code, 0, 0
-    need(state_in is not None, 10, "a state pool needs state_in")
+    if state_in is None:
+        raise KdaError(10, "a state pool needs state_in")
     if state_in.dim() != 3 or state_in.shape[0] < 1:
         raise KdaError(2, f"a state pool needs state_in [slots, {a}, {b}]")
     slots = state_in.shape[0]
@@ -167,7 +177,7 @@ def states(state_in, state_out, state_dtype, io_dtype, N, a, b, ssm_state_indice
                       ("state_out_indices", state_out_indices)):
         if ids is not None:
             is_tensor(ids, name, torch.int32)
-            if ids.shape != (N,) or not ids.is_contiguous():
+            if ids.dim() != 1 or ids.numel() != N or not ids.is_contiguous():
                 raise KdaError(2, f"{name} must be a contiguous [{N}]")
     return state_in, state_dtype, code, slots, pitch
 
@@ -176,5 +186,5 @@ def vector(t, name, n):
     """An optional FP32 [n]."""
     if t is not None:
         is_tensor(t, name, _torch.float32)
-        if t.shape != (n,) or not t.is_contiguous():
+        if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
             raise KdaError(2, f"{name} must be a contiguous [{n}]")

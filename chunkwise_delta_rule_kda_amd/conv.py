@@ -5,7 +5,7 @@ import ctypes
 
 from . import KdaError, kda_last_error, load_library
 from ._tensors import (channel_strides, contiguous_like, dtype_code, get_torch, is_tensor,
-                       on_device, run_on, sequences, states, vector)
+                       new_state, on_device, run_on, sequences, states, vector)
 
 __all__ = ["kda_short_conv", "kda_short_conv_args", "kda_short_conv_check",
            "make_short_conv_args"]
@@ -96,7 +96,7 @@ def kda_short_conv(x, weight, bias=None, state_in=None, cu_seqlens=None, *, acti
         if out is None:
             out = contiguous_like(x)
         if state_out is None and output_final_state:
-            state_out = x.new_empty((N, W - 1, C), dtype=state_dtype)
+            state_out = new_state(x, state_in, (N, W - 1, C), state_dtype)
         a = kda_short_conv_args(
             x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state_in), _ptr(cu_seqlens),
             out.data_ptr(), _ptr(state_out), B, T, C, W, N, xb, xt, io, st, _ACT[activation],

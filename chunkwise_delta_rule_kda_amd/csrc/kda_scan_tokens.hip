@@ -66,7 +66,7 @@ __global__ __launch_bounds__(256) void scan_tokens_kernel(ScanParams p, int64_t 
     const int64_t at = mine + j * (kSide * N);
     h[j] = A[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     if (c0 + j * kSide >= p.D) continue;
-    if (in >= 0) h[j] = p.state.bf16 ? load4<true>(p.state.in, in + at) : load4<false>(p.state.in, in + at);
+    if (in >= 0) h[j] = p.state.bf16 ? load_once4<true>(p.state.in, in + at) : load_once4<false>(p.state.in, in + at);
     A[j] = load4<false>(p.A, at);
   }
   const float bias = p.bias ? p.bias[c] : 0.f, skip = p.skip ? p.skip[c] : 0.f;
@@ -115,8 +115,8 @@ __global__ __launch_bounds__(256) void scan_tokens_kernel(ScanParams p, int64_t 
   for (int j = 0; j < NC; ++j) {
     const int64_t at = out + mine + j * (kSide * N);
     if (c0 + j * kSide >= p.D) continue;
-    if (p.state.bf16) store4<true>(p.state.out, at, h[j]);
-    else store4<false>(p.state.out, at, h[j]);
+    if (p.state.bf16) store_once4<true>(p.state.out, at, h[j]);
+    else store_once4<false>(p.state.out, at, h[j]);
   }
 }
 

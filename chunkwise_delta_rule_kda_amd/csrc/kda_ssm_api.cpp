@@ -280,9 +280,9 @@ kda_status scan_sizes(const kda_selective_scan_args* a, ScanPlan* pl) {
   if (rows * a->D > (Wide(1) << 50) || (rows / 64 + a->N) * dense > (Wide(1) << 50))
     return fail(KDA_ERR_SHAPE, "B*T*D or N*D*S is out of range");
   *pl = scan_plan(a);
-  const Wide wgs = pl->tokens ? static_cast<Wide>(a->N) * ceil_div(a->D, 1024 / a->S)
-                              : static_cast<Wide>(pl->slots) * pl->cblocks + 16;
-  if (wgs * 256 > kMaxThreads) return fail(KDA_ERR_SHAPE, "too much for one launch (N*D, or segments*D)");
+  const Wide threads = pl->tokens ? static_cast<Wide>(a->N) * ceil_div(a->D, 1024 / a->S) * 256
+                                  : (static_cast<Wide>(pl->slots) * pl->cblocks + 16) * 512;
+  if (threads > kMaxThreads) return fail(KDA_ERR_SHAPE, "too much for one launch (N*D, or segments*D)");
   return KDA_OK;
 }
 
@@ -433,7 +433,6 @@ kda_status kda_selective_scan(const kda_selective_scan_args* a, void* stream_) {
   }
   p.softplus = (a->flags & KDA_SCAN_SOFTPLUS) != 0;
   p.state = state_slots(a, a->D * a->S);
-  if (p.N == 0) return KDA_OK;
   if (pl.tokens) return done(kda::launch_scan_tokens(p, n, bf16, stream));
   p.seg_len = pl.seg ? pl.seg : a->T + 1;  // longer than any sequence: a slot for each
   p.segs_per_seq = pl.segs;

@@ -4,7 +4,7 @@ import ctypes
 
 from . import KdaError, _raise_if, kda_last_error, load_library
 from ._tensors import (channel_strides, contiguous_like, dtype_code, get_torch, is_tensor, need,
-                       on_device, run_on, sequences, states, vector)
+                       new_state, on_device, run_on, sequences, states, vector)
 
 __all__ = ["kda_selective_scan", "kda_selective_scan_args", "kda_selective_scan_check",
            "kda_selective_scan_plan", "kda_selective_scan_workspace_bytes",
@@ -129,15 +129,15 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
     grouped = B.dim() == 4
     G = B.shape[2] if grouped else 1
     rows = (batch, T, G, S) if grouped else (batch, T, S)
-    st = []
-    for name, t in (("B", B), ("C", C)):
-        if t.shape != rows:
-            raise KdaError(2, f"{name} has shape {tuple(t.shape)}, expected {rows}")
-        s = t.stride()
-        if s[-1] != 1 and batch and T:
-            raise KdaError(2, f"the last axis of {name} must be contiguous")
-        # the stride of an axis of one entry says nothing
-        st += [0 if batch == 1 else s[0], 0 if T == 1 else s[1], 0 if G == 1 else s[2]]
+    if B.shape != rows or C.shape != rows:
+        raise KdaError(2, f"B and C have shapes {tuple(B.shape)} and {tuple(C.shape)}, expected {rows}")
+    sB, sC = B.stride(), C.stride()
+    if (sB[-1] != 1 or sC[-1] != 1) and batch and T:
+        raise KdaError(2, "the last axis of B and C must be contiguous")
+    sB, sC = sB[:3], sC[:3]
+    if batch == 1 or T == 1 or G == 1:  # the stride of an axis of one entry says nothing
+        one = [n == 1 for n in (batch, T, G)]
+        sB, sC = ([0 if o else x for o, x in zip(one, st)] for st in (sB, sC))
     if G < 1 or channels % G:
         raise KdaError(2, f"{G} groups do not divide {channels} channels")
     vector(D, "D", channels)
@@ -162,12 +162,12 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
         if out is None:
             out = contiguous_like(u)
         if state_out is None and output_final_state:
-            state_out = u.new_empty((N, channels, S), dtype=state_dtype)
+            state_out = new_state(u, state_in, (N, channels, S), state_dtype)
         a = kda_selective_scan_args(
             u.data_ptr(), delta.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(),
             _ptr(D), _ptr(delta_bias), _ptr(state_in), _ptr(cu_seqlens), out.data_ptr(),
-            _ptr(state_out), None, 0, batch, T, channels, S, G, N, ub, ut, db, dtok, zb, zt, *st,
-            io, code, _SOFTPLUS if delta_softplus else 0, segment_tokens,
+            _ptr(state_out), None, 0, batch, T, channels, S, G, N, ub, ut, db, dtok, zb, zt, *sB,
+            *sC, io, code, _SOFTPLUS if delta_softplus else 0, segment_tokens,
             _ptr(ssm_state_indices), _ptr(state_out_indices), slots, pitch)
         ref = ctypes.byref(a)
         if workspace is not None:
