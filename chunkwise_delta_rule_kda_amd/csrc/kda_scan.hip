@@ -40,12 +40,12 @@ __device__ __forceinline__ int by_length(const int64_t* cu, int n, int rank) {
 // Workgroups b and b + 8 run on the same XCD one after the other: they get neighbouring
 // channel blocks, whose 64-byte parts of a BF16 row share a cache line.
 __device__ __forceinline__ bool scan_task(const ScanParams& p, ScanTask& t) {
-  const int64_t b = blockIdx.x;
-  const int64_t i = b >> 3;
-  const int64_t task = ((i >> 1) * 8 + (b & 7)) * 2 + (i & 1);
-  const int64_t w = task / p.cblocks;
+  const uint32_t b = blockIdx.x;
+  const uint32_t i = b >> 3;
+  const uint32_t task = ((i >> 1) * 8 + (b & 7)) * 2 + (i & 1);
+  const uint32_t w = task / static_cast<uint32_t>(p.cblocks);
   if (w >= p.slots) return false;
-  t.cblk = static_cast<int>(task - w * p.cblocks);
+  t.cblk = static_cast<int>(task - w * static_cast<uint32_t>(p.cblocks));
   t.slot = w;
   int64_t total = p.T;
   if (p.cu_seqlens) {
@@ -53,9 +53,9 @@ __device__ __forceinline__ bool scan_task(const ScanParams& p, ScanTask& t) {
                           : find_sequence(p.cu_seqlens, p.N, p.seg_len, w);
     t.begin = p.cu_seqlens[t.n];
     total = p.cu_seqlens[t.n + 1] - t.begin;
-    t.seg = p.longest_first ? 0 : w - (t.begin / p.seg_len + t.n);
+    t.seg = p.longest_first ? 0 : w - (divide(t.begin, p.seg_len) + t.n);
   } else {
-    t.n = w / p.segs_per_seq;
+    t.n = divide(w, p.segs_per_seq);
     t.begin = 0;
     t.seg = w - t.n * p.segs_per_seq;
   }
@@ -251,7 +251,7 @@ struct ScanLoader {
     z_stride = p.z ? p.zs[1] : p.us[1];
     out = static_cast<char*>(p.out) + ((n * p.T + t.row0 - kScanTile) * p.D + c0) * kElem;
     out_at = (static_cast<uint32_t>(tok) * static_cast<uint32_t>(p.D) + quad) * kElem;
-    const int64_t group = c0 / p.per_group;
+    const int64_t group = divide(c0, p.per_group);
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {

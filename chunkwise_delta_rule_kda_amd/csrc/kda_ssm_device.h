@@ -9,6 +9,12 @@ namespace kda {
 // LDS operations are complete and all waves here; loads from memory stay in flight.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
+// a / b of numbers that are not negative, and mostly fit 32 bits.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // The sequence that slot w belongs to where sequence n has the slots from cu[n] / len + n on:
 // the last n with cu[n] / len + n <= w, 64 candidates at a time. w is uniform over the wave.
 __device__ __forceinline__ int64_t find_sequence(const int64_t* cu, int64_t n, int64_t len,
@@ -18,7 +24,7 @@ __device__ __forceinline__ int64_t find_sequence(const int64_t* cu, int64_t n, i
   while (size > 1) {
     const int64_t step = (size + 63) / 64;
     const int64_t at = lo + lane * step;
-    const bool ok = lane * step < size && cu[at] / len + at <= w;
+    const bool ok = lane * step < size && divide(cu[at], len) + at <= w;
     const int c = __popcll(__ballot(ok));
     const int64_t skip = (c > 0 ? c - 1 : 0) * step;
     lo += skip;

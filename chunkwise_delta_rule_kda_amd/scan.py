@@ -113,7 +113,7 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
     if delta.shape != shape:
         raise KdaError(2, f"delta has shape {tuple(delta.shape)}, expected {tuple(shape)}")
     ub, ut = channel_strides(u, "u", batch, T)
-    db, dtok = channel_strides(delta, "delta", batch, T)
+    db, dt_ = channel_strides(delta, "delta", batch, T)
     zb = zt = 0
     if z is not None:
         is_tensor(z, "z", dt)
@@ -134,10 +134,10 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
     sB, sC = B.stride(), C.stride()
     if (sB[-1] != 1 or sC[-1] != 1) and batch and T:
         raise KdaError(2, "the last axis of B and C must be contiguous")
-    sB, sC = sB[:3], sC[:3]
-    if batch == 1 or T == 1 or G == 1:  # the stride of an axis of one entry says nothing
-        one = [n == 1 for n in (batch, T, G)]
-        sB, sC = ([0 if o else x for o, x in zip(one, st)] for st in (sB, sC))
+    # the stride of an axis of one entry says nothing
+    Bb, Cb = (0, 0) if batch == 1 else (sB[0], sC[0])
+    Bt, Ct = (0, 0) if T == 1 else (sB[1], sC[1])
+    Bg, Cg = (0, 0) if G == 1 else (sB[2], sC[2])
     if G < 1 or channels % G:
         raise KdaError(2, f"{G} groups do not divide {channels} channels")
     vector(D, "D", channels)
@@ -166,8 +166,8 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
         a = kda_selective_scan_args(
             u.data_ptr(), delta.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(),
             _ptr(D), _ptr(delta_bias), _ptr(state_in), _ptr(cu_seqlens), out.data_ptr(),
-            _ptr(state_out), None, 0, batch, T, channels, S, G, N, ub, ut, db, dtok, zb, zt, *sB,
-            *sC, io, code, _SOFTPLUS if delta_softplus else 0, segment_tokens,
+            _ptr(state_out), None, 0, batch, T, channels, S, G, N, ub, ut, db, dt_, zb, zt, Bb, Bt,
+            Bg, Cb, Ct, Cg, io, code, _SOFTPLUS if delta_softplus else 0, segment_tokens,
             _ptr(ssm_state_indices), _ptr(state_out_indices), slots, pitch)
         ref = ctypes.byref(a)
         if workspace is not None:
