@@ -299,3 +299,67 @@ def test_other_stream_graph_and_repeat(T, seg):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(end, want_end)
+
+
+@pytest.mark.parametrize("B,D,S,G,io,st", [
+    (70, 1928, 16, 1, "bf16", "fp32"),   # the last wave's channels partly behind the end
+    (70, 1920, 16, 30, "bf16", "bf16"),  # a row of B and C for each wave of 64 channels
+    (66, 2016, 16, 63, "fp32", "fp32"),  # for each 32 channels: less than a wave has
+    (70, 1928, 8, 1, "bf16", "fp32"),
+    (70, 1000, 32, 1, "fp32", "bf16"),
+    (35, 968, 64, 1, "bf16", "fp32"),
+])
+@pytest.mark.parametrize("T", [1, 3])
+def test_many_tokens(B, D, S, G, io, st, T):
+    """Calls large enough for several channels in a lane of the token form."""
+    check(inputs(B, T, D, S, G, io, st), f"scan {B} x {T} tokens, {D} channels, {S} states")
+
+
+def test_rows_behind_the_last_sequence_stay():
+    import torch
+
+    for seg in (-1, 64):
+        d = inputs(1, 150, 72, lens=[70, 0, 50], steps=(1e-3, 0.1))
+        out = torch.full((1, 150, 72), 7.0, device="cuda", dtype=torch.bfloat16)
+        y, s = run(d, out=out, segment_tokens=seg)
+        assert bool((y[:, 120:] == 7).all())
+        first = {n: d[n][:, :120] for n in ("u", "delta", "B", "C", "z")}
+        y2, s2 = run(dict(d, **first), segment_tokens=seg)
+        assert torch.equal(y[:, :120], y2) and torch.equal(s, s2)
+
+
+def test_two_streams_at_once():
+    import torch
+
+    d = [inputs(2, 600, 136, seed=i) for i in range(2)]
+    want = [run(x, segment_tokens=64) for x in d]
+    streams = [torch.cuda.Stream() for _ in d]
+    torch.cuda.synchronize()
+    import chunkwise_delta_rule_kda_amd as kda
+
+    got = []
+    for _ in range(4):
+        for x, s in zip(d, streams):
+            a = dict(x, stream=s, segment_tokens=64)
+            first = [a.pop(n) for n in ("u", "delta", "A", "B", "C")]
+            got.append(kda.kda_selective_scan(*first, **a))
+    torch.cuda.synchronize()
+    for i, (y, s) in enumerate(got):
+        assert torch.equal(y, want[i % 2][0]) and torch.equal(s, want[i % 2][1])
+
+
+def test_automatic_geometry_of_long_prompts():
+    """The segments that the library takes by itself, against the oracle."""
+    import chunkwise_delta_rule_kda_amd as kda
+
+    for lens in (None, [3000, 1, 1096]):
+        d = inputs(1, 4097, 40, lens=lens, steps=(1e-3, 0.1), io="fp32")
+        N = 1 if lens is None else 3
+        plan = kda.kda_selective_scan_plan(kda.make_selective_scan_args(
+            B=1, T=4097, D=40, N=N, io_dtype=1, state_dtype=1, flags=1,
+            cu_seqlens=None if lens is None else d["cu_seqlens"]))
+        assert plan["segment_tokens"] > 0
+        y, s = run(d)
+        y_ref, s_ref, y_err, s_err = oracle(d, segment=plan["segment_tokens"])
+        within(y, y_ref, y_err, f"scan 4097 tokens {lens} out")
+        within(s, s_ref, s_err, f"scan 4097 tokens {lens} state")

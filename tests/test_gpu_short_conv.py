@@ -249,3 +249,35 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(end, want_end)
+
+
+def test_rows_behind_the_last_sequence_stay():
+    import torch
+
+    d = inputs(1, 90, 136, lens=[40, 0, 30])
+    out = torch.full((1, 90, 136), 7.0, device="cuda", dtype=torch.bfloat16)
+    y, s = run(d, out=out)
+    assert bool((y[:, 70:] == 7).all())
+    y2, s2 = run(dict(d, x=d["x"][:, :70]))
+    assert torch.equal(y[:, :70], y2) and torch.equal(s, s2)
+
+
+def test_large_call():
+    """More than 64 million elements: shorter runs of a thread. Sixteen channels of each end and the
+    middle against the definition."""
+    import torch
+
+    d = inputs(1, 8192, 8200, 4)
+    y, s = run(d)
+    pick = torch.tensor([*range(16), *range(4096, 4112), *range(8184, 8200)], device="cuda")
+    part = dict(d, x=d["x"][..., pick], weight=d["weight"][pick], bias=d["bias"][pick],
+                state_in=d["state_in"][..., pick])
+    y_ref, s_ref, err = oracle(part)
+    check_out(y[..., pick], y_ref, err, "conv 8192 x 8200")
+    assert torch.equal(s[..., pick].cpu(), torch.from_numpy(s_ref).float().to(s.dtype))
+    # every element at least finite, and each row like that of a short call from its window
+    assert bool(torch.isfinite(y).all())
+    for t in (7, 8, 4095, 8190):
+        state = d["x"][:, t - 3:t].contiguous()
+        one, _ = run(dict(d, x=d["x"][:, t:t + 1], state_in=state))
+        assert torch.equal(one[:, 0], y[:, t])
