@@ -4,7 +4,7 @@
 // A thread takes eight channels (one 16-byte piece of a BF16 row) of a run of tokens of one
 // sequence and keeps the last W - 1 rows in registers, so a row is read once, and W - 1 rows
 // a second time where a run begins. Bound by its bytes, buffers in turn: 8192 x 36864 BF16, 1209
-// MB in 220 us (5.5 TB/s, a copy of as much 228); FP32 packed, 221 MB in 43 us (5.2 TB/s, the
+// MB in 217 us (5.6 TB/s, a copy of as much 228); FP32 packed, 221 MB in 43 us (5.2 TB/s, the
 // copy 42); 8192 x 2304 BF16, 76 MB in 20 us (the copy 16).
 
 #include "kda_ssm_device.h"

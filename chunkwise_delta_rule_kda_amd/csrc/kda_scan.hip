@@ -5,14 +5,14 @@
 // multiplications, an exponential and two fused multiply-adds of the vector units.
 //
 // A workgroup has 32 channels of one sequence (or of one time segment of it). Four waves hold
-// the states of eight channels each: lane L has channel L % 8 and the n / 8 states of group
-// L / 8, in registers for the whole run. Four others bring tiles of 32 tokens through LDS,
+// the states of eight channels each: lane L has channel L / 4 % 8 and the n / 8 states of
+// group L % 4 + 4 (L / 32), in registers for the whole run. Four others bring tiles of 32 tokens through LDS,
 // twice buffered, with one barrier each: u, delta, z, B and C come from memory two tiles ahead,
 // delta becomes d and d u, and the outputs of the tile before are finished.
 //
 // Bound by the vector units: of 612 issue slots that a SIMD spends on a tile (N = 16) 397 are the
 // recurrence, 68 the sums over the lanes, 146 the loaders'; 8 x 1024 x 4096 BF16 in 132 us, with
-// the units busy all the time. 8192 x 8192 in one run, a workgroup on each compute unit: 324 us,
+// the units busy all the time. 8192 x 8192 in one run, a workgroup on each compute unit: 319 us,
 // 80 % busy. All waves in turn at loading and scanning took 542 there, LDS reads just before their
 // use 364.
 
@@ -161,8 +161,9 @@ struct ScanStates {
 
   __device__ __forceinline__ void run(ScanTile<N, OUT>& tile, int column, int g, int64_t left) {
     if (left >= kScanTile) {
-      // LDS is read ahead; the compiler by itself would read just before the use
-      constexpr int kAhead = NS <= 2 ? 4 : NS == 4 ? 2 : 1;
+      // LDS is read ahead; the compiler by itself would read just before the use. 8192 x 8192:
+      // four tokens ahead 324 us, two 319
+      constexpr int kAhead = NS <= 4 ? 2 : 1;  // tokens
       float r[kScanTile][ScanTile<N, OUT>::kBC], y[8];
       f32x2 dx[kScanTile / 4];
       dx[0] = load_dx(tile, column, 0);
@@ -179,12 +180,7 @@ struct ScanStates {
           __builtin_amdgcn_sched_barrier(0);
           float* out = &y[t % 8];
           const f32x2 v = dx[t4 / 4];
-          if constexpr (kAhead == 4) {
-            out[0] = token<0>(v, r[t]);
-            out[1] = token<1>(v, r[t + 1]);
-            out[2] = token<2>(v, r[t + 2]);
-            out[3] = token<3>(v, r[t + 3]);
-          } else if constexpr (kAhead == 2) {
+          if constexpr (kAhead == 2) {
             out[0] = j == 0 ? token<0>(v, r[t]) : token<2>(v, r[t]);
             out[1] = j == 0 ? token<1>(v, r[t + 1]) : token<3>(v, r[t + 1]);
           } else {

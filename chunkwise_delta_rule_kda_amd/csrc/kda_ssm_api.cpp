@@ -206,7 +206,7 @@ ScanPlan scan_plan(const kda_selective_scan_args* a) {
   // (8, and 0.2 for each segment whose end a start state has to come through).
   // One sequence of 8192 tokens, S = 16: D = 768 314 serial, 56 by segments of 256 or 384, 64
   // by 832; D = 1536 316, 95 (384, 512), 104 (832); D = 4096 320, 227 (512), 242 (1664); D =
-  // 8192 322, 394 by two segments. T = 512, D = 1536: 23.5 serial, 17.8 by segments of 64.
+  // 8192 319, 394 by two segments. T = 512, D = 1536: 23.5 serial, 17.8 by segments of 64.
   const bool bf16 = a->io_dtype == KDA_BF16;
   const double states = static_cast<double>(a->S);
   const double alone = 0.5 + 0.047 * states + (bf16 ? 0 : 0.15), shared = 0.4 + 0.04 * states + (bf16 ? 0 : 0.15);
