@@ -3,6 +3,8 @@ stream and device a call runs on. These calls can take a few microseconds on the
 the checks of the common case are kept short."""
 
 import contextlib
+import ctypes
+import struct
 
 from . import KDA_BF16, KDA_FP32, KdaError
 
@@ -46,11 +48,16 @@ def is_tensor(t, name, dtype=None):
 def on_device(first, names, *rest):
     """All tensors (or None) are on the first one's CUDA device; names: of all of them."""
     index = first.get_device() if first.is_cuda else -1
+    for t in rest:
+        if t is not None and t.get_device() != index:
+            break
+    else:
+        if index >= 0:
+            return first.device
     for i, t in enumerate((first, *rest)):
         if t is not None and (index < 0 or t.get_device() != index):
             raise KdaError(2, f"{names.split()[i]} must be a CUDA tensor on "
                            f"{first.device if index >= 0 else 'cuda'} (got {t.device})")
-    return first.device
 
 
 def contiguous_like(t):
@@ -93,6 +100,17 @@ def run_on(device, stream):
     if stream is None and _torch.cuda.current_device() == device.index:
         return _Current(_raw_stream(device.index))
     return _on(device, stream)
+
+
+def packer(args):
+    """A function that makes the bytes of an argument structure from all of its fields, in
+    order (pointers as integers): filling the ctypes structure itself takes three times as
+    long, and a call of few tokens takes as long as its host side."""
+    codes = {ctypes.c_void_p: "P", ctypes.c_size_t: "N", ctypes.c_int64: "q", ctypes.c_int32: "i"}
+    made = struct.Struct("@" + "".join(codes[kind] for _, kind in args._fields_))
+    if made.size != ctypes.sizeof(args):
+        raise TypeError(f"{args.__name__} ends in padding")
+    return made.pack
 
 
 def new_state(like, state_in, shape, dtype):
@@ -147,13 +165,16 @@ def states(state_in, state_out, state_dtype, io_dtype, N, a, b, ssm_state_indice
     if ssm_state_indices is None:
         if state_out_indices is not None:
             raise KdaError(10, "state_out_indices needs ssm_state_indices")
-        if state_out is not None:
+        shape = (N, a, b)
+        if state_in is not None:
+            _state_check(state_in, "state_in", shape, state_dtype)
+            if not state_in.is_contiguous():
+                raise KdaError(2, "state_in must be contiguous")
+        if state_out is not None and state_out is not state_in:
             is_tensor(state_out, "state_out")
-        for name, t in (("state_in", state_in), ("state_out", state_out)):
-            if t is not None:
-                _state_check(t, name, (N, a, b), state_dtype)
-                if not t.is_contiguous():
-                    raise KdaError(2, f"{name} must be contiguous")
+            _state_check(state_out, "state_out", shape, state_dtype)
+            if not state_out.is_contiguous():
+                raise KdaError(2, "state_out must be contiguous")
         return state_out, state_dtype, code, 0, 0
     if state_in is None:
         raise KdaError(10, "a state pool needs state_in")
@@ -177,7 +198,7 @@ def states(state_in, state_out, state_dtype, io_dtype, N, a, b, ssm_state_indice
                       ("state_out_indices", state_out_indices)):
         if ids is not None:
             is_tensor(ids, name, torch.int32)
-            if ids.dim() != 1 or ids.numel() != N or not ids.is_contiguous():
+            if ids.shape != (N,) or not ids.is_contiguous():
                 raise KdaError(2, f"{name} must be a contiguous [{N}]")
     return state_in, state_dtype, code, slots, pitch
 
@@ -186,5 +207,5 @@ def vector(t, name, n):
     """An optional FP32 [n]."""
     if t is not None:
         is_tensor(t, name, _torch.float32)
-        if t.dim() != 1 or t.numel() != n or not t.is_contiguous():
+        if t.shape != (n,) or not t.is_contiguous():
             raise KdaError(2, f"{name} must be a contiguous [{n}]")

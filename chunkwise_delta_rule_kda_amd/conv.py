@@ -5,7 +5,7 @@ import ctypes
 
 from . import KdaError, kda_last_error, load_library
 from ._tensors import (channel_strides, contiguous_like, dtype_code, get_torch, is_tensor,
-                       new_state, on_device, run_on, sequences, states, vector)
+                       new_state, on_device, packer, run_on, sequences, states, vector)
 
 __all__ = ["kda_short_conv", "kda_short_conv_args", "kda_short_conv_check",
            "make_short_conv_args"]
@@ -22,6 +22,9 @@ class kda_short_conv_args(ctypes.Structure):
         + [(n, _I32) for n in ("io_dtype", "state_dtype", "flags")]
         + [("ssm_state_indices", _P), ("state_out_indices", _P), ("state_pool_slots", _I64),
            ("state_slot_pitch", _I64)])
+
+
+_pack = packer(kda_short_conv_args)
 
 
 def _ptr(x):
@@ -97,11 +100,13 @@ def kda_short_conv(x, weight, bias=None, state_in=None, cu_seqlens=None, *, acti
             out = contiguous_like(x)
         if state_out is None and output_final_state:
             state_out = new_state(x, state_in, (N, W - 1, C), state_dtype)
-        a = kda_short_conv_args(
-            x.data_ptr(), weight.data_ptr(), _ptr(bias), _ptr(state_in), _ptr(cu_seqlens),
-            out.data_ptr(), _ptr(state_out), B, T, C, W, N, xb, xt, io, st, _ACT[activation],
-            _ptr(ssm_state_indices), _ptr(state_out_indices), slots, pitch)
-        status = load_library().kda_short_conv(ctypes.byref(a), handle)
+        a = _pack(
+            *[0 if t is None else t.data_ptr() for t in (
+                x, weight, bias, state_in, cu_seqlens, out, state_out)],
+            B, T, C, W, N, xb, xt, io, st, _ACT[activation],
+            0 if ssm_state_indices is None else ssm_state_indices.data_ptr(),
+            0 if state_out_indices is None else state_out_indices.data_ptr(), slots, pitch)
+        status = load_library().kda_short_conv(a, handle)
     if status:
         raise KdaError(status, kda_last_error())
     return out, state_out

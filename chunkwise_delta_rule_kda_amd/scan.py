@@ -4,7 +4,7 @@ import ctypes
 
 from . import KdaError, _raise_if, kda_last_error, load_library
 from ._tensors import (channel_strides, contiguous_like, dtype_code, get_torch, is_tensor, need,
-                       new_state, on_device, run_on, sequences, states, vector)
+                       new_state, on_device, packer, run_on, sequences, states, vector)
 
 __all__ = ["kda_selective_scan", "kda_selective_scan_args", "kda_selective_scan_check",
            "kda_selective_scan_plan", "kda_selective_scan_workspace_bytes",
@@ -26,6 +26,9 @@ class kda_selective_scan_args(ctypes.Structure):
         + [(n, _I32) for n in ("io_dtype", "state_dtype", "flags")]
         + [("segment_tokens", _I64), ("ssm_state_indices", _P), ("state_out_indices", _P),
            ("state_pool_slots", _I64), ("state_slot_pitch", _I64)])
+
+
+_pack = packer(kda_selective_scan_args)
 
 
 class kda_selective_scan_plan_info(ctypes.Structure):
@@ -130,7 +133,8 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
     G = B.shape[2] if grouped else 1
     rows = (batch, T, G, S) if grouped else (batch, T, S)
     if B.shape != rows or C.shape != rows:
-        raise KdaError(2, f"B and C have shapes {tuple(B.shape)} and {tuple(C.shape)}, expected {rows}")
+        raise KdaError(2, f"B and C have shapes {tuple(B.shape)} and {tuple(C.shape)}, "
+                       f"expected {rows}")
     sB, sC = B.stride(), C.stride()
     if (sB[-1] != 1 or sC[-1] != 1) and batch and T:
         raise KdaError(2, "the last axis of B and C must be contiguous")
@@ -163,23 +167,23 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
             out = contiguous_like(u)
         if state_out is None and output_final_state:
             state_out = new_state(u, state_in, (N, channels, S), state_dtype)
-        a = kda_selective_scan_args(
-            u.data_ptr(), delta.data_ptr(), _ptr(z), B.data_ptr(), C.data_ptr(), A.data_ptr(),
-            _ptr(D), _ptr(delta_bias), _ptr(state_in), _ptr(cu_seqlens), out.data_ptr(),
-            _ptr(state_out), None, 0, batch, T, channels, S, G, N, ub, ut, db, dt_, zb, zt, Bb, Bt,
-            Bg, Cb, Ct, Cg, io, code, _SOFTPLUS if delta_softplus else 0, segment_tokens,
-            _ptr(ssm_state_indices), _ptr(state_out_indices), slots, pitch)
-        ref = ctypes.byref(a)
-        if workspace is not None:
-            a.workspace = workspace.data_ptr()
-            a.workspace_bytes = workspace.numel() * workspace.element_size()
-        status = lib.kda_selective_scan(ref, handle)
+        a = _pack(
+            *[0 if t is None else t.data_ptr() for t in (
+                u, delta, z, B, C, A, D, delta_bias, state_in, cu_seqlens, out, state_out,
+                workspace)],
+            0 if workspace is None else workspace.numel() * workspace.element_size(),
+            batch, T, channels, S, G, N, ub, ut, db, dt_, zb, zt, Bb, Bt, Bg, Cb, Ct, Cg, io, code,
+            _SOFTPLUS if delta_softplus else 0, segment_tokens,
+            0 if ssm_state_indices is None else ssm_state_indices.data_ptr(),
+            0 if state_out_indices is None else state_out_indices.data_ptr(), slots, pitch)
+        status = lib.kda_selective_scan(a, handle)
         if status == 7 and workspace is None:  # the call needs one: refused before any launch
+            a = kda_selective_scan_args.from_buffer_copy(a)
             workspace = torch.empty(kda_selective_scan_workspace_bytes(a), dtype=torch.uint8,
                                     device=dev)
             a.workspace = workspace.data_ptr()
             a.workspace_bytes = workspace.numel()
-            status = lib.kda_selective_scan(ref, handle)
+            status = lib.kda_selective_scan(ctypes.byref(a), handle)
     if status:
         raise KdaError(status, kda_last_error())
     return out, state_out
