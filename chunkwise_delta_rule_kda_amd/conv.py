@@ -58,11 +58,14 @@ def kda_short_conv(x, weight, bias=None, state_in=None, cu_seqlens=None, *, acti
         y_t[c] = act(bias[c] + sum_i weight[c, i] x_{t - (W-1) + i}[c]),  i = 0 .. W-1
 
     in fp32, rounded once. x: [B, T, C], bf16 or fp32, C a multiple of 8; only its last axis
-    has to be contiguous (the other strides multiples of 8), so q, k and v side by side, or
-    one part of a projection, are taken as they are. weight: fp32 [C, W] with W 2, 3 or 4;
-    bias: fp32 [C] or None. activation: "silu" or None.
+    has to be contiguous (the other strides multiples of 8, the tokens' at most 2^22), so q, k
+    and v side by side, or one part of a projection, are taken as they are. weight: fp32 [C, W]
+    with W 2, 3 or 4; bias: fp32 [C] or None. Tensors start on multiples of 16 bytes.
+    activation: "silu" or None.
     state_in: [N, W - 1, C], the inputs before each sequence, the oldest first, or None
-    (zeros); state_out=state_in updates in place. cu_seqlens: int64 [N + 1] (B = 1) or None.
+    (zeros); state_out=state_in updates in place. state_dtype: the states' type, bf16 or fp32;
+    None is state_in's, or without one x's, in which they are exact. cu_seqlens: int64 [N + 1]
+    (B = 1) or None.
     ssm_state_indices (int32 [N]): state_in is a pool [slots, W - 1, C] (its first axis may be
     padded), sequence n starts from slot ssm_state_indices[n] and writes its final state to
     slot state_out_indices[n] (None: the slot it read); the returned state is the pool. Ids

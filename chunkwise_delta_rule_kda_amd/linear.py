@@ -92,7 +92,8 @@ def kda_linear(q, k, v, g=None, state_in=None, cu_seqlens=None, *, log_decay=Non
     projection are taken as they are. g: [B, T, H] log decays (<= 0; -inf empties the
     state) of q's dtype or fp32, or None. log_decay: fp32 [H], a fixed decay of each head,
     or None; where both are given they add. scale: None (or 0) is 1 / sqrt(K).
-    state_in: [N, H, V, K] or None (zeros); state_out=state_in updates in place.
+    state_in: [N, H, V, K] or None (zeros); state_out=state_in updates in place. state_dtype:
+    the states' type, bf16 or fp32; None is state_in's, or without one q's.
     cu_seqlens: int64 [N + 1] (B = 1) or None.
     1 <= T <= 8 in the fixed layout is the step of single (or a few draft) tokens: each state
     is read and written once. segment_tokens: 0 automatic, negative serial, positive the

@@ -93,9 +93,13 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
     or 64. B, C: [B, T, S], or [B, T, G, S] where channel c reads group c // (channels // G)
     (groups of a multiple of 32 channels). D, delta_bias: fp32 [channels] or None.
     delta_softplus=False takes delta + delta_bias as the step size. Of u, delta, z, B and C
-    only the last axis has to be contiguous (the other strides multiples of 8), so slices of
-    projections are taken as they are.
+    only the last axis has to be contiguous (the other strides multiples of 8, the tokens' at
+    most 2^22), so slices of projections are taken as they are. Tensors other than D and
+    delta_bias start on multiples of 16 bytes.
     state_in: [N, channels, S] or None (zeros); state_out=state_in updates in place.
+    state_dtype: the states' type, bf16 or fp32; None is state_in's, or without one u's. With
+    bf16 inputs ask for torch.float32 where the state is carried from call to call: a bf16 one
+    is rounded in each, and under a decay closer to 1 than 2^-9 it does not move at all.
     cu_seqlens: int64 [N + 1] (B = 1) or None. 1 <= T <= 8 in the fixed layout is the step of
     single (or a few draft) tokens: each state is read and written once. segment_tokens: 0
     automatic, negative serial, positive the time-segment length (a multiple of 64).

@@ -585,7 +585,8 @@ typedef struct kda_short_conv_args {
 
   int64_t B, T, C, W, N; /* C a multiple of 8 up to 2^22; W 2, 3 or 4 */
   int64_t x_stride[2];   /* batch, token in elements; not negative, multiples of 8, a token
-                            stride of at most 2^22 */
+                            stride of at most 2^22. x, out, weight, bias and the states are
+                            16-byte aligned */
   int32_t io_dtype;      /* kda_dtype of x and out */
   int32_t state_dtype;   /* kda_dtype of state_in and state_out */
   int32_t flags;         /* KDA_CONV_* */
@@ -646,10 +647,13 @@ typedef struct kda_selective_scan_args {
   int64_t B, T, D, S, G, N; /* D a multiple of 8 up to 2^22; S 8, 16, 32 or 64; G divides D,
                                groups of a multiple of 32 channels unless G is 1 */
   /* Strides in elements: batch, token (and group). Not negative, multiples of 8, a token
-     stride of at most 2^22. */
+     stride of at most 2^22. u, delta, z, B_in, C_in, A, out and the states are 16-byte
+     aligned. */
   int64_t u_stride[2], delta_stride[2], z_stride[2], B_stride[3], C_stride[3];
   int32_t io_dtype;    /* kda_dtype of u, delta, z, B_in, C_in and out */
-  int32_t state_dtype; /* kda_dtype of state_in and state_out */
+  int32_t state_dtype; /* kda_dtype of state_in and state_out. A BF16 state is rounded at the
+                          end of each call: carried through calls of a token each, it does
+                          not move under a decay closer to 1 than 2^-9 */
   int32_t flags;       /* KDA_SCAN_* */
 
   /* Time segments: tokens per segment (a positive multiple of 64), 0 = automatic,

@@ -154,3 +154,30 @@ def test_rows_past_31_bits():
         assert torch.equal(y[:, -64:], want) and torch.equal(y[:, :64], want)
         assert torch.equal(s[1:], end) and not y[:, 64:-64].any()
         del y, s
+
+
+def test_state_types_of_calls_without_a_state():
+    """state_dtype as documented: the inputs' type unless asked for. And what the documentation
+    warns of: carried in BF16 under decays closer to 1 than 2^-9 a state stands still (half a
+    unit of its last place is at least 2^-9 of it), in FP32 it follows the recurrence."""
+    import torch
+
+    import chunkwise_delta_rule_kda_amd as kda
+
+    d = inputs(2, 1, 72, state=False, softplus=False)
+    call = lambda state, **kw: kda.kda_selective_scan(
+        d["u"], d["delta"], d["A"], d["B"], d["C"], d["D"], d["z"], state, delta_softplus=False, **kw)[1]
+    assert call(None).dtype == torch.bfloat16
+    assert call(None, state_dtype=torch.float32).dtype == torch.float32
+    x, w = d["u"], torch.ones(72, 4, device="cuda")
+    assert kda.kda_short_conv(x, w)[1].dtype == torch.bfloat16
+    assert kda.kda_short_conv(x, w, state_dtype=torch.float32)[1].dtype == torch.float32
+    d["u"], d["delta"], d["A"] = d["u"] * 0, d["delta"] * 0 + 1, d["A"] * 0 - 2.0 ** -10
+    first = torch.randn(2, 72, 16, device="cuda").bfloat16()
+    few, full = first, first.float()
+    for _ in range(200):
+        few, full = call(few), call(full)
+    assert torch.equal(few, first)
+    want = first.double() * torch.exp(torch.tensor(-200 * 2.0 ** -10, dtype=torch.float64))
+    # a token's exponential is off by 3 units of 2^-24 at most, its product by one
+    assert bool(((full.double() - want).abs() <= 200 * 4 * 2.0 ** -24 * want.abs()).all())
