@@ -102,7 +102,10 @@ def kda_selective_scan(u, delta, A, B, C, D=None, z=None, state_in=None, cu_seql
     is rounded in each, and under a decay closer to 1 than 2^-9 it does not move at all.
     cu_seqlens: int64 [N + 1] (B = 1) or None. 1 <= T <= 8 in the fixed layout is the step of
     single (or a few draft) tokens: each state is read and written once. segment_tokens: 0
-    automatic, negative serial, positive the time-segment length (a multiple of 64).
+    automatic, negative serial, positive the time-segment length (a multiple of 64). Packed
+    lengths are known on the device only, and the automatic rule takes the longest for 1.75
+    times the mean: where one prompt is packed with many short sequences, pass a length
+    (1536 channels, 8000 tokens and 63 single ones: 119 us with 512, 312 without).
     ssm_state_indices (int32 [N]): state_in is a pool [slots, channels, S] (its first axis may
     be padded), sequence n starts from slot ssm_state_indices[n] and writes its final state
     to slot state_out_indices[n] (None: the slot it read); the returned state is the pool.

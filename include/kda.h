@@ -659,7 +659,10 @@ typedef struct kda_selective_scan_args {
   /* Time segments: tokens per segment (a positive multiple of 64), 0 = automatic,
      negative = one serial run per sequence. With segments, their end states are formed
      first, in parallel, then all outputs, in parallel, each from the ends before it. Results
-     differ from the serial form only by rounding. */
+     differ from the serial form only by rounding. The automatic rule does not know a packed
+     batch's lengths and takes the longest for 1.75 times the mean: for one prompt among many
+     short sequences give a length (one of 8000 tokens and 63 of one, D = 1536, S = 16: 119 us
+     with 512, 312 without). */
   int64_t segment_tokens;
 
   /* State pool: as in kda_linear_args. */
