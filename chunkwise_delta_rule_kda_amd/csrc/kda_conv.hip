@@ -3,9 +3,10 @@
 // whose rows before the sequence are its state, and the state behind it: the last W - 1 rows.
 // A thread takes eight channels (one 16-byte piece of a BF16 row) of a run of tokens of one
 // sequence and keeps the last W - 1 rows in registers, so a row is read once, and W - 1 rows
-// a second time where a run begins. Bound by its bytes, buffers in turn: 8192 x 36864 BF16, 1209
-// MB in 217 us (5.6 TB/s, a copy of as much 228); FP32 packed, 221 MB in 43 us (5.2 TB/s, the
-// copy 42); 8192 x 2304 BF16, 76 MB in 20 us (the copy 16).
+// a second time where a run begins. Bound by its bytes, inputs and outputs in turn: 8192 x 36864
+// BF16, 1209 MB in 216 us (5.6 TB/s, a copy of as much 227); FP32 packed, 221 MB in 52 us (4.3
+// TB/s, the copy 42; 45 where each call writes the memory that the last one wrote, which the
+// last-level cache then holds); 8192 x 2304 BF16, 76 MB in 18.3 us (the copy 16).
 
 #include "kda_ssm_device.h"
 
@@ -63,8 +64,8 @@ __global__ __launch_bounds__(256) void conv_kernel(ConvParams p, uint32_t blocks
   const int64_t w = static_cast<int64_t>(row) * (256 / LANES) + threadIdx.x / LANES;
 
   // All loads are on their way before the first wait: the taps', the first rows' and, of BF16, the
-  // rows before those (8192 x 36864: 217 us, 220 with these behind the taps; FP32, whose rows
-  // take twice the registers, packed 45.5 and 43).
+  // rows before those (8192 x 36864: 216 us, 223 with these behind the taps; FP32, whose rows
+  // take twice the registers, packed 45.0 and 44.8).
   constexpr int kTaps = (LANES * 8 * W + 1023) / 1024;  // pieces of four of this thread
   const int count = static_cast<int>(octets - octet0 < LANES ? octets - octet0 : LANES) * 8 * W;
   f32x4 piece[kTaps];

@@ -12,7 +12,7 @@
 //
 // Bound by the vector units: of 612 issue slots that a SIMD spends on a tile (N = 16) 397 are the
 // recurrence, 68 the sums over the lanes, 146 the loaders'; 8 x 1024 x 4096 BF16 in 132 us, with
-// the units busy all the time. 8192 x 8192 in one run, a workgroup on each compute unit: 319 us,
+// the units busy all the time. 8192 x 8192 in one run, a workgroup on each compute unit: 318 us,
 // 80 % busy. All waves in turn at loading and scanning took 542 there, LDS reads just before their
 // use 364.
 
@@ -117,8 +117,12 @@ __device__ __forceinline__ float reduce8(const float (&v)[8]) {
   return (odd ? b[1] : b[0]) + quad_lanes<0xB1>(odd ? b[0] : b[1]);
 }
 
-constexpr int kYRow = kScanChannels + 8;      // floats of an LDS row of y, and of a pair of
-constexpr int kDxRow = 4 * kScanChannels + 4; // tokens' step sizes: no two rows' banks meet
+// Floats of an LDS row of y, and of a pair of tokens' step sizes. What a wave writes is spread
+// evenly over the banks. The two rows of step sizes that its quads read share 28 of their 32
+// banks; rows of 164 floats, which share none, take the same time (8 x 1024 x 4096 131.7 us and
+// 131.9, 8192 x 8192 317.8 and 317.7).
+constexpr int kYRow = kScanChannels + 8;
+constexpr int kDxRow = 4 * kScanChannels + 4;
 
 // A tile in LDS.
 template <int N, bool OUT>
@@ -162,7 +166,7 @@ struct ScanStates {
   __device__ __forceinline__ void run(ScanTile<N, OUT>& tile, int column, int g, int64_t left) {
     if (left >= kScanTile) {
       // LDS is read ahead; the compiler by itself would read just before the use. 8192 x 8192:
-      // four tokens ahead 324 us, two 319
+      // four tokens ahead 324 us, two 318
       constexpr int kAhead = NS <= 4 ? 2 : 1;  // tokens
       float r[kScanTile][ScanTile<N, OUT>::kBC], y[8];
       f32x2 dx[kScanTile / 4];

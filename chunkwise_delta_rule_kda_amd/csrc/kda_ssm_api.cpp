@@ -117,8 +117,8 @@ struct ConvPlan {
 ConvPlan conv_plan(const kda_short_conv_args* a) {
   ConvPlan pl{};
   // Tokens of a thread: longer runs read fewer rows twice, shorter ones keep what is in flight
-  // closer together. BF16, 8192 rows, 8 and 16 tokens: 2304 channels 22.0 and 20.1 us, 9216 61.1
-  // and 61.6, 36864 220 and 227 (32 tokens: 241); FP32, 2304 channels: 32.3 and 36.4.
+  // closer together. BF16, 8192 rows, 8 and 16 tokens: 2304 channels 21.4 and 20.0 us, 9216 59.9
+  // and 60.7, 36864 216 and 225 (32 tokens: 239); FP32, 2304 channels: 32.3 and 35.5.
   const bool few = a->io_dtype == KDA_BF16 && static_cast<Wide>(a->B) * a->T * a->C <= 64000000;
   pl.run = a->T <= 1 && !a->cu_seqlens ? 1 : few ? 16 : 8;
   pl.runs_per_seq = a->T > 0 ? ceil_div(a->T, pl.run) : 1;
@@ -205,8 +205,11 @@ ScanPlan scan_plan(const kda_selective_scan_args* a) {
   // steps, or all workgroups' over 256 compute units. Segments: two launches of all of them
   // (8, and 0.2 for each segment whose end a start state has to come through).
   // One sequence of 8192 tokens, S = 16: D = 768 314 serial, 56 by segments of 256 or 384, 64
-  // by 832; D = 1536 316, 95 (384, 512), 104 (832); D = 4096 320, 227 (512), 242 (1664); D =
-  // 8192 319, 394 by two segments. T = 512, D = 1536: 23.5 serial, 17.8 by segments of 64.
+  // by 832; D = 1536 316, 97 (384, 512), 104 (832); D = 4096 320, 227 (512), 242 (1664); D =
+  // 8192 318, 394 by two segments. T = 512, D = 1536: 23.5 serial, 17.8 by segments of 64.
+  // A packed batch of 64 sequences, 8063 tokens, D = 1536: even lengths 74 serial, 79 by segments
+  // of 1024; one of 8000 tokens 312 serial, which is what the guess of its longest one gives,
+  // 119 by segments of 512.
   const bool bf16 = a->io_dtype == KDA_BF16;
   const double states = static_cast<double>(a->S);
   const double alone = 0.5 + 0.047 * states + (bf16 ? 0 : 0.15), shared = 0.4 + 0.04 * states + (bf16 ? 0 : 0.15);
