@@ -1,12 +1,14 @@
 """kda_selective_scan in the geometries that its own tests leave out: several groups of B and C
 with segments and packed batches, more than two blocks of 32 channels with segments, step sizes
 at both ends carried over segments, packed batches about the bound up to which the longest
-sequence runs first, one long sequence among many short ones, and offsets past 2^32. Every case
-that means segments asserts them on the plan.
+sequence runs first, one long sequence among many short ones, offsets past 2^32, calls without
+tokens in pools, very many sequences, and captured packed calls whose lengths change. Every
+case that means segments asserts them on the plan.
 
 Tolerance: as in test_gpu_selective_scan.py, the oracle's bound on FP32 arithmetic and the
 result's own rounding, element by element."""
 
+import numpy as np
 import pytest
 
 from test_gpu_selective_scan import _gpu, check, dtype, inputs, oracle, run, within  # noqa: F401
@@ -181,3 +183,67 @@ def test_state_types_of_calls_without_a_state():
     want = first.double() * torch.exp(torch.tensor(-200 * 2.0 ** -10, dtype=torch.float64))
     # a token's exponential is off by 3 units of 2^-24 at most, its product by one
     assert bool(((full.double() - want).abs() <= 200 * 4 * 2.0 ** -24 * want.abs()).all())
+
+
+@pytest.mark.parametrize("S", [8, 32])
+def test_no_tokens_in_a_pool(S):
+    import torch
+
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    ids = dict(ssm_state_indices=i32([2, 2, 9]), state_out_indices=i32([6, 0, 4]))
+    for lens in (None, [0, 0, 0]):
+        d = inputs(1 if lens else 3, 0, 72, S, lens=lens, state=False)
+        pool = torch.randn(7, 72, S, device="cuda")
+        want = pool.clone()
+        want[[6, 0]] = pool[[2, 2]]
+        want[4] = 0
+        run(dict(d, state_in=pool), **ids)
+        assert torch.equal(pool, want)
+
+
+def test_very_many_sequences():
+    import torch
+
+    d = inputs(70001, 1, 8)
+    y, s = run(d)
+    pick = [0, 1, 4095, 4096, 65535, 65536, 70000]
+    part = dict(d, **{n: d[n][pick] for n in ("u", "delta", "B", "C", "z", "state_in")})
+    y_ref, s_ref, y_err, s_err = oracle(part)
+    within(y[pick], y_ref, y_err, "scan 70001 tokens out")
+    within(s[pick], s_ref, s_err, "scan 70001 tokens state")
+    assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(s).all())
+    lens = [int(n) for n in np.random.default_rng(2).integers(0, 4, 5000)]
+    lens[4321] = 200
+    d = inputs(1, sum(lens), 8, lens=lens)
+    check(d, "scan packed 5000 sequences", segment_tokens=-1)
+    segmented(d, "scan packed 5000 sequences, segments", 64)
+
+
+@pytest.mark.parametrize("seg", [-1, 64])
+def test_captured_packed_call_with_other_lengths(seg):
+    """The lengths are read on the device: a captured call follows them, cut or not."""
+    import torch
+
+    import chunkwise_delta_rule_kda_amd as kda
+
+    d = inputs(1, 250, 72, lens=[70, 0, 180])
+    out, end = torch.empty_like(d["u"]), torch.empty_like(d["state_in"])
+    call = lambda: kda.kda_selective_scan(
+        d["u"], d["delta"], d["A"], d["B"], d["C"], d["D"], d["z"], d["state_in"], d["cu_seqlens"],
+        delta_bias=d["delta_bias"], out=out, state_out=end, segment_tokens=seg)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for cu in ([0, 0, 249, 250], [0, 250, 250, 250], [0, 63, 128, 250]):
+        d["cu_seqlens"].copy_(torch.tensor(cu))
+        d["u"].copy_(torch.randn_like(d["u"]))
+        want, want_end = run(d, segment_tokens=seg)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(end, want_end)

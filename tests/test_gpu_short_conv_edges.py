@@ -1,10 +1,10 @@
-"""kda_short_conv with offsets past 32 bits: sequences and slots more than 2^31 elements apart,
-and a call of more than 2^31 elements. Tolerances as in test_gpu_short_conv.py."""
+"""kda_short_conv at its edges: offsets past 32 bits, calls without tokens, very many sequences,
+and captured packed calls whose lengths change. Tolerances as in test_gpu_short_conv.py."""
 
 import numpy as np
 import pytest
 
-from test_gpu_short_conv import _gpu, check_out, host, inputs, oracle, run  # noqa: F401
+from test_gpu_short_conv import _gpu, check, check_out, host, inputs, oracle, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,66 @@ def test_rows_past_31_bits():
         assert torch.equal(part, y[:, a:a + 40])
     assert torch.equal(s[0], x[0, 97:100]) and torch.equal(s[2], x[0, T - 3:])
     assert torch.equal(s[1, 2], x[0, 100]) and not s[1, :2].any()
+
+
+@pytest.mark.parametrize("io,st,W", [("bf16", "fp32", 4), ("fp32", "bf16", 2)])
+def test_no_tokens(io, st, W):
+    """States pass a call of no tokens: dense, in place, and from slot to slot of a pool."""
+    import torch
+
+    d = inputs(3, 0, 72, W, io, st)
+    y, s = run(d)
+    assert y.shape == (3, 0, 72) and torch.equal(s, d["state_in"])
+    kept = d["state_in"].clone()
+    _, s = run(d, state_out=d["state_in"])
+    assert torch.equal(s, kept) and not run(dict(d, state_in=None))[1].any()
+    pool = torch.randn(7, W - 1, 72, device="cuda").to(kept.dtype)
+    want = pool.clone()
+    want[[6, 0]] = pool[[2, 2]]
+    want[4] = 0
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    run(d, state_in=pool, ssm_state_indices=i32([2, 2, 9]), state_out_indices=i32([6, 0, 4]))
+    assert torch.equal(pool, want)
+
+
+@pytest.mark.parametrize("C", [8, 40])
+def test_very_many_sequences(C):
+    import torch
+
+    d = inputs(70001, 1, C)
+    y, s = run(d)
+    pick = [0, 1, 4095, 4096, 65535, 65536, 70000]
+    part = dict(d, x=d["x"][pick], state_in=d["state_in"][pick])
+    y_ref, s_ref, err = oracle(part)
+    check_out(y[pick], y_ref, err, "conv 70001 tokens")
+    assert np.array_equal(host(s[pick]), s_ref) and bool(torch.isfinite(y).all())
+    rng = np.random.default_rng(C)
+    lens = [int(n) for n in rng.integers(0, 4, 5000)]  # 64 candidates at a time, three times
+    check(inputs(1, sum(lens), C, lens=lens), f"conv packed 5000 sequences, {C} channels")
+
+
+def test_captured_packed_call_with_other_lengths():
+    import torch
+
+    import chunkwise_delta_rule_kda_amd as kda
+
+    d = inputs(1, 150, 136, lens=[70, 0, 80])
+    out, end = torch.empty_like(d["x"]), torch.empty_like(d["state_in"])
+    call = lambda: kda.kda_short_conv(d["x"], d["weight"], d["bias"], d["state_in"],
+                                      d["cu_seqlens"], out=out, state_out=end)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for cu in ([0, 0, 149, 150], [0, 150, 150, 150], [0, 15, 32, 150]):
+        d["cu_seqlens"].copy_(torch.tensor(cu))
+        d["x"].copy_(torch.randn_like(d["x"]))
+        want, want_end = run(d)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(end, want_end)
